@@ -16,6 +16,14 @@ loaded, importing the functions below raises.
     st = AdamW8State.zeros(A32.numel(), A32.device)
     adamw8_step(A32.view(-1), dA.view(-1), st, t, lr=2e-4, param_bf16=A.view(-1))
 
+Beside the linear, in modules of their own: ``norm`` (RMS norm with the
+residual addition, its backward, and the same norm with 8-bit output), ``int8``
+(the linear in 8-bit integers that serves a merged weight), ``grads`` (global
+gradient norm and clipping):
+
+    total, coef = grads.norm([dA, dB, ...], max_norm=0.3)
+    adamw8_step(A32.view(-1), dA.view(-1), st, t, lr=2e-4, grad_scale=coef)
+
 The C declarations, with argument meaning, layout and error behaviour, are
 in include/qlora_nf4.h.
 """
@@ -48,6 +56,11 @@ class _Weight(ctypes.Structure):
                 ("dq_step", ctypes.c_void_p), ("dq_mean", ctypes.c_void_p)]
 
 
+class _TensorList(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int), ("data", ctypes.POINTER(ctypes.c_void_p)),
+                ("n", ctypes.POINTER(ctypes.c_int64)), ("dtype", ctypes.POINTER(ctypes.c_int))]
+
+
 _lib = None
 
 
@@ -63,6 +76,7 @@ def lib():
     vp, i64, sz, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
     u64 = ctypes.c_uint64
     wp = ctypes.POINTER(_Weight)
+    tl = ctypes.POINTER(_TensorList)
     sig = {
         "qn_abi_version": (i32, []),
         "qn_status_string": (ctypes.c_char_p, [i32]),
@@ -86,6 +100,16 @@ def lib():
         "lora_dropout": (i32, [vp, i64, i64, f32, u64, u64, vp, vp, vp]),
         "qlora_adamw8_blocks": (sz, [i64]),
         "qlora_adamw8_step": (i32, [vp, vp, i64, vp, vp, vp, vp, vp, f32, f32, f32, f32, f32, i64, vp]),
+        "qlora_adamw8_step_scaled": (i32, [vp, vp, vp, i64, vp, vp, vp, vp, vp, f32, f32, f32, f32, f32, i64, vp]),
+        "qlora_grad_norm_workspace_bytes": (sz, [i32]),
+        "qlora_grad_norm": (i32, [tl, f32, vp, vp, vp, sz, vp]),
+        "qlora_grad_clip": (i32, [tl, tl, vp, vp]),
+        "rmsnorm_fwd": (i32, [vp, vp, vp, i64, i64, f32, vp, vp, vp, vp]),
+        "rmsnorm_fwd_int8": (i32, [vp, vp, vp, i64, i64, f32, vp, vp, vp, vp]),
+        "rmsnorm_bwd_workspace_bytes": (sz, [i64, i64]),
+        "rmsnorm_bwd": (i32, [vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, sz, vp]),
+        "int8_quantize_rows": (i32, [vp, i64, i64, vp, vp, vp]),
+        "int8_linear_fwd": (i32, [vp, vp, i64, vp, vp, i64, i64, vp, vp]),
         "qlora_dropout_workspace_bytes": (sz, [i64, i64, i64, i32]),
         "qlora_linear_fwd_dropout": (i32, [vp, i64, wp, vp, vp, i32, f32, f32, u64, u64, vp, vp, vp, vp,
                                            vp, sz, vp]),
@@ -113,6 +137,32 @@ def _check(status, what):
         if status == 5:
             what = f"{what} [{lib().qn_last_error_string().decode()}]"
         raise QNError(status, what)
+
+
+def _arg(t, what, dtype, shape, device=None):
+    """Refuses a tensor argument that the library cannot take; returns its
+    address (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {dtype} cuda tensor is needed, got {t.dtype} on {t.device}, "
+                         f"strides {t.stride()}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what}: is on {t.device}, the other tensors are on {device}")
+    return t.data_ptr()
+
+
+def _run(name, device, *args):
+    """Calls `name` with the current stream of `device` (made current for the call)."""
+    fn = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    _check(status, name)
 
 
 def levels():
@@ -338,14 +388,19 @@ class AdamW8State:
 
 
 def adamw8_step(param, grad, state, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0,
-                param_bf16=None):
+                param_bf16=None, grad_scale=None):
     """One AdamW step with 8-bit states on the fp32 tensor param (in place),
-    writing bf16(param) into param_bf16 when given."""
+    writing bf16(param) into param_bf16 when given.  grad_scale: None, or one
+    fp32 value on the device that multiplies the gradient (the clipping
+    coefficient of grads.norm)."""
     n = param.numel()
-    _check(lib().qlora_adamw8_step(_ptr(param), _ptr(grad), n, _ptr(state.m_codes), _ptr(state.m_scale),
-                                   _ptr(state.v_codes), _ptr(state.v_scale), _ptr(param_bf16), float(lr),
-                                   float(beta1), float(beta2), float(eps), float(weight_decay), int(step),
-                                   _stream()), "qlora_adamw8_step")
+    if grad_scale is not None and (grad_scale.dtype is not torch.float32 or grad_scale.numel() != 1
+                                   or grad_scale.device != param.device):
+        raise ValueError(f"grad_scale: one fp32 value on {param.device} is needed")
+    _check(lib().qlora_adamw8_step_scaled(_ptr(param), _ptr(grad), _ptr(grad_scale), n, _ptr(state.m_codes),
+                                          _ptr(state.m_scale), _ptr(state.v_codes), _ptr(state.v_scale),
+                                          _ptr(param_bf16), float(lr), float(beta1), float(beta2), float(eps),
+                                          float(weight_decay), int(step), _stream()), "qlora_adamw8_step")
 
 
 # ------------------------------------------------------------------ failure detection

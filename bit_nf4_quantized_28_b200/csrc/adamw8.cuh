@@ -8,6 +8,9 @@
 // AdamW (decoupled weight decay), in fp32 one IEEE operation at a time:
 //   m = b1 m0 + (1 - b1) g          v = b2 v0 + (1 - b2) g g
 //   p1 = p (1 - lr wd)               p2 = p1 - ss (m / (sqrt(v) rb + eps))
+// (g first multiplied by a factor in device memory where the caller gives
+// one: the clipping coefficient of the global gradient norm, so that clipping
+// costs no pass of its own)
 // with the bias corrections in two host constants, ss = lr / (1 - b1^t) and
 // rb = 1 / sqrt(1 - b2^t): one square root and one division per value.
 // The states are stored per block of 256 values as one fp32 scale
@@ -37,6 +40,7 @@ struct AdamW8Params {
   uint8_t* vc;               // [n] E4M3 codes of v
   float* vs;                 // [ceil(n / 256)] scales of v
   __nv_bfloat16* pb;         // [n] bf16 copy of p, or null
+  const float* gscale;       // factor of the gradient (clipping), or null
   int64_t n;
   float b1, omb1, b2, omb2, step_size, rsqrt_bc2, decay, eps;
 };
@@ -54,6 +58,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw8_kernel(AdamW8Params p) {
   pdl_launch_dependents();
   pdl_wait_primary();
   const int lane = threadIdx.x & 31;
+  const float gs = p.gscale ? *p.gscale : 1.f;      // (a product with 1 changes no bit)
   const int64_t nblk = (p.n + kAdamBlock - 1) / kAdamBlock;
   const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * kAdamThreads) >> 5;
   for (int64_t b = (static_cast<int64_t>(blockIdx.x) * kAdamThreads + threadIdx.x) >> 5; b < nblk; b += nwarps) {
@@ -93,7 +98,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw8_kernel(AdamW8Params p) {
     for (int j = 0; j < 8; ++j) {
       const float m0 = __fmul_rn(e4m3_value(mcv[j]), msc);
       const float v0 = __fmul_rn(e4m3_value(vcv[j]), vsc);
-      const float g = gv[j];
+      const float g = __fmul_rn(gv[j], gs);
       mn[j] = __fadd_rn(__fmul_rn(p.b1, m0), __fmul_rn(p.omb1, g));
       vn[j] = __fadd_rn(__fmul_rn(p.b2, v0), __fmul_rn(p.omb2, __fmul_rn(g, g)));
       const float p1 = __fmul_rn(pv[j], p.decay);

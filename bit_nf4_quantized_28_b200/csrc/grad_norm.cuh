@@ -1,0 +1,195 @@
+// grad_norm.cuh -- the global norm of many gradient tensors, and clipping.
+//
+//   norm = sqrt(sum over all tensors of g^2),
+//   coef = min(1, max_norm / (norm + 1e-6)),   clipped g = g coef.
+//
+// The tensors (fp32 or bf16, any sizes and element-aligned addresses) are cut
+// into chunks of 4096 values; a CTA takes a contiguous run of the chunks of
+// the whole list, so tensors of very different sizes load every CTA alike.
+// The list travels in the kernel's parameters: no table in device memory.
+// Squares and sums are fp64: they neither overflow (fp32 squares do beyond
+// 1.8e19) nor lose small gradients beside large ones.  The CTAs' sums are
+// added in a fixed order, so equal inputs give equal bits.  HBM-bound: each
+// gradient is read once.
+#pragma once
+
+#include "common.cuh"
+
+namespace qn {
+
+constexpr int kListMax = 1024;        // tensors per launch: 21 KB of the 32,764 bytes of parameters
+constexpr int kChunk = 4096;          // values
+constexpr int kNormThreads = 256;
+
+struct GradList {
+  const void* data[kListMax];
+  int64_t n[kListMax];
+  uint32_t end[kListMax];             // chunks of tensors 0 .. i, with bit 31 = bf16
+  int count;
+};
+
+// Values of the tensor that lie before the first 16-byte boundary are taken
+// with the first chunk: chunk c of a tensor holds values
+// [c kChunk - off, (c + 1) kChunk - off), off = how far its address is past a
+// 16-byte boundary, in values.
+__host__ __device__ inline int list_off(const void* p, bool half) {
+  const int b = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
+  return half ? b >> 1 : b >> 2;
+}
+
+// The tensor that holds chunk c of the list.
+__device__ __forceinline__ int list_find(const GradList& L, uint32_t c) {
+  int lo = 0, hi = L.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if ((L.end[mid] & 0x7FFFFFFFu) > c) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ double sq(float f) {
+  const double d = static_cast<double>(f);
+  return d * d;
+}
+
+// Values [lo, hi) of a chunk that may be cut at either end, one at a time.
+template <typename F>
+__device__ __forceinline__ void each_value(int64_t lo, int64_t hi, F f) {
+  for (int64_t e = lo + threadIdx.x; e < hi; e += kNormThreads) f(e);
+}
+
+__global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(const __grid_constant__ GradList L, double* part) {
+  __shared__ double wsum[kNormThreads / 32];
+  const uint32_t total = L.end[L.count - 1] & 0x7FFFFFFFu;
+  const uint32_t c0 = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / gridDim.x);
+  const uint32_t c1 = static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / gridDim.x);
+  double s = 0.0;
+  int i = c0 < c1 ? list_find(L, c0) : 0;
+  for (uint32_t c = c0; c < c1; ++c) {
+    while ((L.end[i] & 0x7FFFFFFFu) <= c) ++i;
+    const uint32_t first = i ? (L.end[i - 1] & 0x7FFFFFFFu) : 0u;
+    const bool half = (L.end[i] >> 31) != 0u;
+    const int64_t n = L.n[i];
+    const int64_t b = static_cast<int64_t>(c - first) * kChunk - list_off(L.data[i], half);
+    const bool whole = b >= 0 && b + kChunk <= n;
+    if (half) {
+      const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(L.data[i]);
+      if (whole) {
+        const uint4* v = reinterpret_cast<const uint4*>(g + b);
+#pragma unroll
+        for (int k = 0; k < kChunk / 8 / kNormThreads; ++k) {
+          const uint4 u = v[threadIdx.x + k * kNormThreads];
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s += sq(__uint_as_float(w[j] << 16)) + sq(__uint_as_float(w[j] & 0xFFFF0000u));
+        }
+      } else {
+        each_value(b < 0 ? 0 : b, min(b + kChunk, n), [&](int64_t e) { s += sq(__bfloat162float(g[e])); });
+      }
+    } else {
+      const float* g = static_cast<const float*>(L.data[i]);
+      if (whole) {
+        const float4* v = reinterpret_cast<const float4*>(g + b);
+        float4 u[kChunk / 4 / kNormThreads];
+#pragma unroll
+        for (int k = 0; k < kChunk / 4 / kNormThreads; ++k) u[k] = v[threadIdx.x + k * kNormThreads];
+#pragma unroll
+        for (int k = 0; k < kChunk / 4 / kNormThreads; ++k) s += (sq(u[k].x) + sq(u[k].y)) + (sq(u[k].z) + sq(u[k].w));
+      } else {
+        each_value(b < 0 ? 0 : b, min(b + kChunk, n), [&](int64_t e) { s += sq(g[e]); });
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if ((threadIdx.x & 31) == 0) wsum[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kNormThreads / 32; ++w) s += wsum[w];
+    part[blockIdx.x] = s;
+  }
+}
+
+// norm and coef from the CTAs' sums (count of them; 0: no values, norm 0).
+__global__ void __launch_bounds__(kNormThreads) grad_norm_finish_kernel(const double* part, int count, float max_norm,
+                                                                        float* norm, float* coef) {
+  __shared__ double wsum[kNormThreads / 32];
+  pdl_wait_primary();
+  double s = 0.0;
+  for (int i = threadIdx.x; i < count; i += kNormThreads) s += part[i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if ((threadIdx.x & 31) == 0) wsum[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kNormThreads / 32; ++w) s += wsum[w];
+    const float r = static_cast<float>(sqrt(s));
+    *norm = r;
+    if (coef) {
+      const float c = __fdiv_rn(max_norm, r + 1e-6f);
+      *coef = c >= 1.f ? 1.f : c;      // a NaN norm gives a NaN coefficient
+    }
+  }
+}
+
+struct GradOut {
+  void* data[kListMax];
+};
+
+// out = g coef, rounded once to the tensors' type, chunk by chunk.
+__global__ void __launch_bounds__(kNormThreads) grad_clip_kernel(const __grid_constant__ GradList L,
+                                                                 const __grid_constant__ GradOut O,
+                                                                 const float* coef) {
+  const float f = *coef;
+  const uint32_t total = L.end[L.count - 1] & 0x7FFFFFFFu;
+  const uint32_t c0 = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / gridDim.x);
+  const uint32_t c1 = static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / gridDim.x);
+  int i = c0 < c1 ? list_find(L, c0) : 0;
+  for (uint32_t c = c0; c < c1; ++c) {
+    while ((L.end[i] & 0x7FFFFFFFu) <= c) ++i;
+    if (f == 1.f && O.data[i] == L.data[i]) continue;     // in place, nothing to clip
+    const uint32_t first = i ? (L.end[i - 1] & 0x7FFFFFFFu) : 0u;
+    const bool half = (L.end[i] >> 31) != 0u;
+    const int64_t n = L.n[i];
+    const int64_t b = static_cast<int64_t>(c - first) * kChunk - list_off(L.data[i], half);
+    // the output may be aligned differently: then one value at a time
+    const bool whole = b >= 0 && b + kChunk <= n && list_off(O.data[i], half) == list_off(L.data[i], half);
+    if (half) {
+      const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(L.data[i]);
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(O.data[i]);
+      if (whole) {
+#pragma unroll
+        for (int k = 0; k < kChunk / 8 / kNormThreads; ++k) {
+          const uint4 u = reinterpret_cast<const uint4*>(g + b)[threadIdx.x + k * kNormThreads];
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          uint32_t r[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            r[j] = pack_bf16x2(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xFFFF0000u) * f);
+          reinterpret_cast<uint4*>(o + b)[threadIdx.x + k * kNormThreads] = make_uint4(r[0], r[1], r[2], r[3]);
+        }
+      } else {
+        each_value(b < 0 ? 0 : b, min(b + kChunk, n),
+                   [&](int64_t e) { o[e] = __float2bfloat16_rn(__bfloat162float(g[e]) * f); });
+      }
+    } else {
+      const float* g = static_cast<const float*>(L.data[i]);
+      float* o = static_cast<float*>(O.data[i]);
+      if (whole) {
+        float4 u[kChunk / 4 / kNormThreads];
+#pragma unroll
+        for (int k = 0; k < kChunk / 4 / kNormThreads; ++k)
+          u[k] = reinterpret_cast<const float4*>(g + b)[threadIdx.x + k * kNormThreads];
+#pragma unroll
+        for (int k = 0; k < kChunk / 4 / kNormThreads; ++k)
+          reinterpret_cast<float4*>(o + b)[threadIdx.x + k * kNormThreads] =
+              make_float4(u[k].x * f, u[k].y * f, u[k].z * f, u[k].w * f);
+      } else {
+        each_value(b < 0 ? 0 : b, min(b + kChunk, n), [&](int64_t e) { o[e] = g[e] * f; });
+      }
+    }
+  }
+}
+
+}  // namespace qn

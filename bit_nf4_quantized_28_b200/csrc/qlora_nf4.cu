@@ -21,9 +21,12 @@
 #include "dropout.cuh"
 #include "gemm_tc.cuh"
 #include "gemv.cuh"
+#include "grad_norm.cuh"
+#include "int8_linear.cuh"
 #include "lora_small.cuh"
 #include "merge.cuh"
 #include "nf4_storage.cuh"
+#include "rmsnorm.cuh"
 
 using namespace qn;
 
@@ -213,6 +216,7 @@ bool tmap_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
 // ------------------------------------------------------------------ checks
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -1193,6 +1197,14 @@ size_t qlora_adamw8_blocks(int64_t n) { return n > 0 ? static_cast<size_t>((n + 
 qn_status qlora_adamw8_step(float* param, const float* grad, int64_t n, uint8_t* m_codes, float* m_scale,
                             uint8_t* v_codes, float* v_scale, void* param_bf16, float lr, float beta1, float beta2,
                             float eps, float weight_decay, int64_t step, qn_stream_t stream) {
+  return qlora_adamw8_step_scaled(param, grad, nullptr, n, m_codes, m_scale, v_codes, v_scale, param_bf16, lr, beta1,
+                                  beta2, eps, weight_decay, step, stream);
+}
+
+qn_status qlora_adamw8_step_scaled(float* param, const float* grad, const float* grad_scale, int64_t n,
+                                   uint8_t* m_codes, float* m_scale, uint8_t* v_codes, float* v_scale,
+                                   void* param_bf16, float lr, float beta1, float beta2, float eps,
+                                   float weight_decay, int64_t step, qn_stream_t stream) {
   clear_detail();
   if (n < 0) return QN_ERR_SHAPE;
   const bool hp_ok = std::isfinite(lr) && lr >= 0.f && std::isfinite(beta1) && beta1 >= 0.f && beta1 < 1.f &&
@@ -1202,7 +1214,8 @@ qn_status qlora_adamw8_step(float* param, const float* grad, int64_t n, uint8_t*
   if (n == 0) return QN_OK;
   if (!param || !grad || !m_codes || !m_scale || !v_codes || !v_scale) return QN_ERR_ARG;
   if (!aligned16(param) || !aligned16(grad) || !aligned16(m_codes) || !aligned16(m_scale) ||
-      !aligned16(v_codes) || !aligned16(v_scale) || (param_bf16 && !aligned16(param_bf16)))
+      !aligned16(v_codes) || !aligned16(v_scale) || (param_bf16 && !aligned16(param_bf16)) ||
+      !aligned4(grad_scale))
     return QN_ERR_ALIGN;
   if (!device_is_sm100()) return QN_ERR_UNSUPPORTED;
   AdamW8Params a = {};
@@ -1213,6 +1226,7 @@ qn_status qlora_adamw8_step(float* param, const float* grad, int64_t n, uint8_t*
   a.vc = v_codes;
   a.vs = v_scale;
   a.pb = static_cast<__nv_bfloat16*>(param_bf16);
+  a.gscale = grad_scale;
   a.n = n;
   // fp64 on the host from the fp32 hyperparameters, rounded once
   const double b1 = beta1, b2 = beta2;
@@ -1412,3 +1426,306 @@ extern "C" qn_status nf4_quantize_noalloc(const void* w_bf16, const qn_nf4_weigh
              static_cast<const float*>(absmax), nblk, out->qscale, out->dq_step, out->dq_mean, ngroups);
   return to_status(e);
 }
+
+// ====================================================================== row-wise operators
+
+namespace {
+
+template <typename P>
+struct RowLaunch {
+  void (*fn)(P);
+  int threads;
+};
+
+// Vectors of 8 values per thread: with few rows as few as fit a CTA (a row's
+// latency counts), else enough for CTAs of at most 256 threads, of which
+// several share an SM and cover one another's reductions.
+int row_nv(int64_t m, int64_t d) {
+  const int64_t nvec = d / 8;
+  const bool many = m >= 2 * static_cast<int64_t>(sm_count());
+  for (int nv = 1; nv < kRowMaxNV; nv *= 2)
+    if (ceil_div(nvec, nv) <= (many ? 256 : row_max_threads(nv))) return nv;
+  return kRowMaxNV;
+}
+
+int row_threads(int64_t d, int nv) { return static_cast<int>(round_up(ceil_div(d / 8, nv), 32)); }
+
+template <bool kRes, bool kNorm, bool kInt8>
+cudaError_t run_rows(const RowParams& p, cudaStream_t st) {
+  const int nv = row_nv(p.m, p.d);
+  void (*fn)(RowParams) = nv == 1   ? row_kernel<1, kRes, kNorm, kInt8>
+                          : nv == 2 ? row_kernel<2, kRes, kNorm, kInt8>
+                          : nv == 4 ? row_kernel<4, kRes, kNorm, kInt8>
+                                    : row_kernel<8, kRes, kNorm, kInt8>;
+  const int64_t grid = std::min<int64_t>(p.m, int64_t{1} << 30);
+  return launch(fn, dim3(static_cast<unsigned>(grid)), dim3(row_threads(p.d, nv)), 0, st, false, p);
+}
+
+qn_status check_rows(int64_t m, int64_t d) {
+  if (m < 0 || d <= 0 || d % 8 != 0 || d > kRowMaxCols) return QN_ERR_SHAPE;
+  return QN_OK;
+}
+
+// CTAs of the backward when it also sums dw: each leaves one row of partial sums.
+int64_t row_bwd_grid(int64_t m) { return std::min<int64_t>(m, 2 * static_cast<int64_t>(sm_count())); }
+
+qn_status norm_checks(const void* x, const void* residual, const void* weight, int64_t m, int64_t d, float eps,
+                      const void* h) {
+  qn_status s = check_rows(m, d);
+  if (s != QN_OK) return s;
+  if (!std::isfinite(eps) || eps < 0.f) return QN_ERR_ARG;
+  if (m == 0) return QN_OK;
+  if (!x || !weight || (residual && !h)) return QN_ERR_ARG;
+  if (!aligned16(x) || !aligned16(weight) || !aligned16(residual) || (residual && !aligned16(h))) return QN_ERR_ALIGN;
+  return QN_OK;
+}
+
+RowParams row_params(const void* x, const void* residual, const void* weight, int64_t m, int64_t d, float eps, void* h) {
+  RowParams p = {};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.res = static_cast<const __nv_bfloat16*>(residual);
+  p.w = static_cast<const __nv_bfloat16*>(weight);
+  p.h = static_cast<__nv_bfloat16*>(h);
+  p.m = m;
+  p.d = static_cast<int>(d);
+  p.eps = eps;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+qn_status rmsnorm_fwd(const void* x, const void* residual, const void* weight, int64_t m, int64_t d, float eps,
+                      void* h, void* y, float* rstd, qn_stream_t stream) {
+  clear_detail();
+  qn_status s = norm_checks(x, residual, weight, m, d, eps, h);
+  if (s != QN_OK || m == 0) return s;
+  if (!y) return QN_ERR_ARG;
+  if (!aligned16(y) || !aligned16(rstd)) return QN_ERR_ALIGN;
+  if (!device_is_sm100()) return QN_ERR_UNSUPPORTED;
+  RowParams p = row_params(x, residual, weight, m, d, eps, h);
+  p.y = static_cast<__nv_bfloat16*>(y);
+  p.rstd = rstd;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return to_status(residual ? run_rows<true, true, false>(p, st) : run_rows<false, true, false>(p, st));
+}
+
+qn_status rmsnorm_fwd_int8(const void* x, const void* residual, const void* weight, int64_t m, int64_t d, float eps,
+                           void* h, int8_t* codes, float* scale, qn_stream_t stream) {
+  clear_detail();
+  qn_status s = norm_checks(x, residual, weight, m, d, eps, h);
+  if (s != QN_OK || m == 0) return s;
+  if (!codes || !scale) return QN_ERR_ARG;
+  if (!aligned16(codes) || !aligned16(scale)) return QN_ERR_ALIGN;
+  if (!device_is_sm100()) return QN_ERR_UNSUPPORTED;
+  RowParams p = row_params(x, residual, weight, m, d, eps, h);
+  p.q = codes;
+  p.scale = scale;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return to_status(residual ? run_rows<true, true, true>(p, st) : run_rows<false, true, true>(p, st));
+}
+
+size_t rmsnorm_bwd_workspace_bytes(int64_t m, int64_t d) {
+  if (m <= 0 || d <= 0) return 0;
+  return align256(static_cast<size_t>(row_bwd_grid(m)) * static_cast<size_t>(d) * sizeof(float));
+}
+
+qn_status rmsnorm_bwd(const void* dy, const void* h, const void* weight, const float* rstd, const void* dh, int64_t m,
+                      int64_t d, void* dx, float* dw, void* ws, size_t ws_bytes, qn_stream_t stream) {
+  clear_detail();
+  qn_status s = check_rows(m, d);
+  if (s != QN_OK) return s;
+  if (m == 0 && !dw) return QN_OK;
+  if (m > 0 && (!dy || !h || !weight || !rstd || !dx)) return QN_ERR_ARG;
+  if (m > 0 && (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(rstd) || !aligned16(dh) ||
+                !aligned16(dx)))
+    return QN_ERR_ALIGN;
+  if (!aligned16(dw)) return QN_ERR_ALIGN;
+  if (dw && m > 0) {
+    if (!ws || ws_bytes < rmsnorm_bwd_workspace_bytes(m, d)) return QN_ERR_WORKSPACE;
+    if (!aligned16(ws)) return QN_ERR_ALIGN;
+  }
+  if (!device_is_sm100()) return QN_ERR_UNSUPPORTED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (m == 0) return to_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(d) * sizeof(float), st));
+  RowBwdParams p = {};
+  p.dy = static_cast<const __nv_bfloat16*>(dy);
+  p.h = static_cast<const __nv_bfloat16*>(h);
+  p.w = static_cast<const __nv_bfloat16*>(weight);
+  p.rstd = rstd;
+  p.dh = static_cast<const __nv_bfloat16*>(dh);
+  p.dx = static_cast<__nv_bfloat16*>(dx);
+  p.part = static_cast<float*>(ws);
+  p.m = m;
+  p.d = static_cast<int>(d);
+  const int nv = row_nv(m, d);
+  const dim3 block(row_threads(d, nv));
+  if (!dw) {
+    void (*fn)(RowBwdParams) = nv == 1   ? row_bwd_kernel<1, false>
+                               : nv == 2 ? row_bwd_kernel<2, false>
+                               : nv == 4 ? row_bwd_kernel<4, false>
+                                         : row_bwd_kernel<8, false>;
+    const int64_t grid = std::min<int64_t>(m, int64_t{1} << 30);
+    return to_status(launch(fn, dim3(static_cast<unsigned>(grid)), block, 0, st, false, p));
+  }
+  void (*fn)(RowBwdParams) = nv == 1   ? row_bwd_kernel<1, true>
+                             : nv == 2 ? row_bwd_kernel<2, true>
+                             : nv == 4 ? row_bwd_kernel<4, true>
+                                       : row_bwd_kernel<8, true>;
+  const int64_t grid = row_bwd_grid(m);
+  cudaError_t e = launch(fn, dim3(static_cast<unsigned>(grid)), block, 0, st, false, p);
+  if (e != cudaSuccess) return to_status(e);
+  return to_status(launch(row_dw_kernel, dim3(static_cast<unsigned>(ceil_div(d, 32))), dim3(256), 0, st, true,
+                          static_cast<const float*>(p.part), dw, static_cast<int>(grid), static_cast<int>(d)));
+}
+
+qn_status int8_quantize_rows(const void* x, int64_t m, int64_t k, int8_t* codes, float* scale, qn_stream_t stream) {
+  clear_detail();
+  qn_status s = check_rows(m, k);
+  if (s != QN_OK || m == 0) return s;
+  if (!x || !codes || !scale) return QN_ERR_ARG;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scale)) return QN_ERR_ALIGN;
+  if (!device_is_sm100()) return QN_ERR_UNSUPPORTED;
+  RowParams p = row_params(x, nullptr, nullptr, m, k, 0.f, nullptr);
+  p.q = codes;
+  p.scale = scale;
+  return to_status(run_rows<false, false, true>(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ====================================================================== 8-bit linear
+
+extern "C" qn_status int8_linear_fwd(const int8_t* x_codes, const float* x_scale, int64_t m, const int8_t* w_codes,
+                                     const float* w_scale, int64_t n, int64_t k, void* y, qn_stream_t stream) {
+  clear_detail();
+  if (m < 0 || n <= 0 || n % 8 != 0 || n > (int64_t{1} << 30) || k <= 0 || k % 16 != 0 || k > kInt8MaxK ||
+      m > (int64_t{1} << 30))
+    return QN_ERR_SHAPE;
+  if (m == 0) return QN_OK;
+  if (!x_codes || !x_scale || !w_codes || !w_scale || !y) return QN_ERR_ARG;
+  if (!aligned16(x_codes) || !aligned16(x_scale) || !aligned16(w_codes) || !aligned16(w_scale) || !aligned16(y))
+    return QN_ERR_ALIGN;
+  if (!device_is_sm100()) return QN_ERR_UNSUPPORTED;
+  Int8Params p = {};
+  p.x = x_codes;
+  p.xs = x_scale;
+  p.w = w_codes;
+  p.ws = w_scale;
+  p.y = static_cast<__nv_bfloat16*>(y);
+  p.m = m;
+  p.n = n;
+  p.k = k;
+  const dim3 grid(static_cast<unsigned>(ceil_div(n, 16)), static_cast<unsigned>(ceil_div(m, 8)));
+  return to_status(launch(int8_vec_kernel, grid, dim3(kInt8VecThreads), 0, reinterpret_cast<cudaStream_t>(stream),
+                          false, p));
+}
+
+// ====================================================================== gradient norm
+
+namespace {
+
+// CTAs of a pass over a list of tensors: a full wave (8 CTAs of 256 threads per SM), or one per chunk.
+int64_t list_grid(int64_t chunks) { return std::min<int64_t>(chunks, 8 * static_cast<int64_t>(sm_count())); }
+
+int64_t list_chunks(const void* p, int64_t n, bool half) {
+  return n > 0 ? ceil_div(n + list_off(p, half), kChunk) : 0;
+}
+
+qn_status check_list(const qn_tensor_list* L) {
+  if (!L || L->count < 0) return QN_ERR_ARG;
+  if (L->count == 0) return QN_OK;
+  if (!L->data || !L->n || !L->dtype) return QN_ERR_ARG;
+  int64_t chunks = 0;
+  for (int i = 0; i < L->count; ++i) {
+    const bool half = L->dtype[i] == QN_BF16;
+    if (!half && L->dtype[i] != QN_F32) return QN_ERR_ARG;
+    if (L->n[i] < 0 || L->n[i] > (int64_t{1} << 42)) return QN_ERR_SHAPE;
+    if (L->n[i] > 0 && !L->data[i]) return QN_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(L->data[i]) & (half ? 1u : 3u)) return QN_ERR_ALIGN;
+    chunks += list_chunks(L->data[i], L->n[i], half);
+  }
+  return chunks < (int64_t{1} << 31) ? QN_OK : QN_ERR_SHAPE;
+}
+
+// The next launch's worth of a list: its tensors with at least one value,
+// from tensor `at` on; the outputs beside them where `out` is given.
+// Returns the number of chunks (0: none left).
+int64_t fill_list(const qn_tensor_list* L, const qn_tensor_list* out, int* at, GradList* g, GradOut* o) {
+  int64_t chunks = 0;
+  g->count = 0;
+  for (; *at < L->count && g->count < kListMax; ++*at) {
+    const int i = *at;
+    if (L->n[i] == 0) continue;
+    const bool half = L->dtype[i] == QN_BF16;
+    chunks += list_chunks(L->data[i], L->n[i], half);
+    const int c = g->count++;
+    g->data[c] = L->data[i];
+    g->n[c] = L->n[i];
+    g->end[c] = static_cast<uint32_t>(chunks) | (half ? 0x80000000u : 0u);
+    if (o) o->data[c] = const_cast<void*>(out->data[i]);
+  }
+  return chunks;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qlora_grad_norm_workspace_bytes(int count) {
+  if (count < 0) return 0;
+  const int64_t launches = std::max<int64_t>(1, ceil_div(count, kListMax));
+  return align256(static_cast<size_t>(launches) * 8 * sm_count() * sizeof(double));
+}
+
+qn_status qlora_grad_norm(const qn_tensor_list* grads, float max_norm, float* norm, float* coef, void* ws,
+                          size_t ws_bytes, qn_stream_t stream) {
+  clear_detail();
+  qn_status s = check_list(grads);
+  if (s != QN_OK) return s;
+  if (!norm || (coef && (!std::isfinite(max_norm) || max_norm < 0.f))) return QN_ERR_ARG;
+  if (!aligned4(norm) || !aligned4(coef)) return QN_ERR_ALIGN;
+  if (!ws || ws_bytes < qlora_grad_norm_workspace_bytes(grads->count)) return QN_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QN_ERR_ALIGN;
+  if (!device_is_sm100()) return QN_ERR_UNSUPPORTED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  double* part = static_cast<double*>(ws);
+  int count = 0, at = 0;
+  GradList g;
+  while (const int64_t chunks = fill_list(grads, nullptr, &at, &g, nullptr)) {
+    const int64_t grid = list_grid(chunks);
+    const cudaError_t e = launch(grad_norm_kernel, dim3(static_cast<unsigned>(grid)), dim3(kNormThreads), 0, st,
+                                 false, g, part + count);
+    if (e != cudaSuccess) return to_status(e);
+    count += static_cast<int>(grid);
+  }
+  return to_status(launch(grad_norm_finish_kernel, dim3(1), dim3(kNormThreads), 0, st, count > 0,
+                          static_cast<const double*>(part), count, max_norm, norm, coef));
+}
+
+qn_status qlora_grad_clip(const qn_tensor_list* grads, const qn_tensor_list* out, const float* coef,
+                          qn_stream_t stream) {
+  clear_detail();
+  qn_status s = check_list(grads);
+  if (s != QN_OK) return s;
+  if (!out) out = grads;
+  s = check_list(out);
+  if (s != QN_OK) return s;
+  if (!coef || out->count != grads->count) return QN_ERR_ARG;
+  if (!aligned4(coef)) return QN_ERR_ALIGN;
+  for (int i = 0; i < grads->count; ++i)
+    if (out->n[i] != grads->n[i] || out->dtype[i] != grads->dtype[i]) return QN_ERR_SHAPE;
+  if (!device_is_sm100()) return QN_ERR_UNSUPPORTED;
+  int at = 0;
+  GradList g;
+  GradOut o;
+  while (const int64_t chunks = fill_list(grads, out, &at, &g, &o)) {
+    const cudaError_t e = launch(grad_clip_kernel, dim3(static_cast<unsigned>(list_grid(chunks))), dim3(kNormThreads),
+                                 0, reinterpret_cast<cudaStream_t>(stream), false, g, o, coef);
+    if (e != cudaSuccess) return to_status(e);
+  }
+  return QN_OK;
+}
+
+}  // extern "C"

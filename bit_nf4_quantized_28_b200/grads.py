@@ -1,0 +1,91 @@
+"""Global gradient norm and clipping, in front of the optimizer step.
+
+    total, coef = norm([dA1, dB1, ...], max_norm=0.3)
+    qn.adamw8_step(p, grad, state, t, lr, grad_scale=coef)    # clips as it reads the gradient
+    clip([dA1, dB1, ...], coef)                               # for another optimizer: in place
+
+coef = min(1, max_norm / (total + 1e-6)); both stay on the device.  A program
+whose gradients live in fixed buffers makes a TensorList of them once (and a
+workspace, which calls on different streams must not share) and passes it
+instead of the list.  Formulas: include/qlora_nf4.h.
+"""
+
+import ctypes
+
+import torch
+
+from . import _run, _TensorList, lib
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+class TensorList:
+    """A fixed list of gradients: contiguous fp32 or bf16 tensors of any
+    shapes on one device.  Holds the tensors; their storage must not be
+    exchanged (set_, resize_) while the list is in use."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("at least one tensor is needed")
+        self.device = self.tensors[0].device
+        for i, t in enumerate(self.tensors):
+            if t.dtype not in _DTYPES or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"tensor {i}: a contiguous float32 or bfloat16 cuda tensor is needed, got {t.dtype} "
+                                 f"on {t.device}, strides {t.stride()}")
+            if t.device != self.device:
+                raise ValueError(f"tensor {i}: is on {t.device}, the others are on {self.device}")
+        c = len(self.tensors)
+        self._data = (ctypes.c_void_p * c)(*(t.data_ptr() for t in self.tensors))
+        self._n = (ctypes.c_int64 * c)(*(t.numel() for t in self.tensors))
+        self._dtype = (ctypes.c_int * c)(*(_DTYPES[t.dtype] for t in self.tensors))
+        self._struct = _TensorList(c, self._data, self._n, self._dtype)
+        self.ref = ctypes.byref(self._struct)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def _as_list(tensors):
+    return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+
+
+def workspace_bytes(tensors):
+    return lib().qlora_grad_norm_workspace_bytes(len(tensors))
+
+
+def make_workspace(tensors):
+    """Workspace of norm for a list of this length."""
+    tensors = _as_list(tensors)
+    return torch.empty(workspace_bytes(tensors), dtype=torch.uint8, device=tensors.device)
+
+
+def norm(tensors, max_norm=None, out=None, workspace=None):
+    """(total, coef): the norm of all tensors together and the factor that
+    clips it to max_norm (None without max_norm), fp32 scalars on the device.
+    out: None or fp32 [2] that receives both."""
+    tensors = _as_list(tensors)
+    dev = tensors.device
+    out = torch.empty(2, dtype=torch.float32, device=dev) if out is None else out
+    if out.dtype is not torch.float32 or out.numel() != 2 or out.device != dev or not out.is_contiguous():
+        raise ValueError(f"out: two fp32 values on {dev} are needed")
+    ws = make_workspace(tensors) if workspace is None else workspace
+    if ws.device != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"workspace: a contiguous uint8 tensor on {dev} is needed")
+    p = out.data_ptr()
+    _run("qlora_grad_norm", dev, tensors.ref, 0.0 if max_norm is None else max_norm, p,
+         None if max_norm is None else p + 4, ws.data_ptr(), ws.numel())
+    return out[0], None if max_norm is None else out[1]
+
+
+def clip(tensors, coef, out=None):
+    """Multiplies every tensor by coef (one fp32 value on the device), in
+    place or into `out`, tensors of the same shapes and types that are each
+    the gradient itself or disjoint from all of them."""
+    tensors = _as_list(tensors)
+    out = None if out is None else _as_list(out)
+    if coef.dtype is not torch.float32 or coef.numel() != 1 or coef.device != tensors.device:
+        raise ValueError(f"coef: one fp32 value on {tensors.device} is needed")
+    if out is not None and out.device != tensors.device:
+        raise ValueError(f"out: is on {out.device}, the gradients are on {tensors.device}")
+    _run("qlora_grad_clip", tensors.device, tensors.ref, None if out is None else out.ref, coef.data_ptr())

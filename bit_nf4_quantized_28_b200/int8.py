@@ -1,0 +1,72 @@
+"""The linear in 8-bit integers: a weight served with one scale per output
+channel, tokens with one scale each.
+
+    w = merge(nf4, A, B, alpha)            # adapter folded into the NF4 weight, then 8 bits
+    w = quantize_weight(W)                 # or any bf16 weight [n_out, k_in]
+    codes, scale = quantize(x)             # tokens (norm.forward_int8 gives them directly)
+    y = linear(codes, scale, w)            # bf16 [m, n_out]
+
+[LoRA y QLoRA en Profundidad, "Cómo Funciona LoRA": for inference the LoRA
+matrices are merged; QLoRA glossary, "QLoRA e metodi correlati": merged 16-bit
+weights are often quantized again for serving.]
+
+k_in % 16 == 0, n_out % 8 == 0; the calls run on the tensors' device, on its
+current stream.  Formulas and rounding: include/qlora_nf4.h.
+"""
+
+from dataclasses import dataclass
+
+import torch
+
+from . import _arg, _run
+from . import merge as _merge
+
+BF16, F32, I8 = torch.bfloat16, torch.float32, torch.int8
+
+
+@dataclass
+class Weight:
+    """A weight [n_out, k_in] as int8 codes and one fp32 scale per row."""
+    n_out: int
+    k_in: int
+    codes: torch.Tensor     # int8 [n_out, k_in]
+    scale: torch.Tensor     # fp32 [n_out]
+
+
+def quantize(x, codes=None, scale=None):
+    """bf16 rows [m, k] -> (codes int8 [m, k], scale fp32 [m]); codes * scale
+    stands for x."""
+    if x.dim() != 2:
+        raise ValueError(f"x: [m, k] is needed, got {tuple(x.shape)}")
+    m, k = x.shape
+    codes = torch.empty(m, k, dtype=I8, device=x.device) if codes is None else codes
+    scale = torch.empty(m, dtype=F32, device=x.device) if scale is None else scale
+    _run("int8_quantize_rows", x.device, _arg(x, "x", BF16, x.shape), m, k, _arg(codes, "codes", I8, x.shape, x.device),
+         _arg(scale, "scale", F32, x.shape[:1], x.device))
+    return codes, scale
+
+
+def quantize_weight(W):
+    """bf16 W [n_out, k_in] -> Weight."""
+    codes, scale = quantize(W)
+    return Weight(W.shape[0], W.shape[1], codes, scale)
+
+
+def merge(w, A=None, B=None, alpha=0.0, out=None):
+    """The NF4 weight with its adapter folded in, W_hat + (alpha / r) B A,
+    rounded to bf16 and then quantized to 8 bits.  out: None or a bf16
+    [n_out, k_in] buffer for the merged weight."""
+    return quantize_weight(_merge(w, A, B, alpha, out=out))
+
+
+def linear(codes, scale, w, y=None):
+    """y = (codes w.codes^T) * scale * w.scale as bf16 [m, n_out]."""
+    if codes.dim() != 2:
+        raise ValueError(f"codes: [m, k] is needed, got {tuple(codes.shape)}")
+    m = codes.shape[0]
+    dev = codes.device
+    y = torch.empty(m, w.n_out, dtype=BF16, device=dev) if y is None else y
+    _run("int8_linear_fwd", dev, _arg(codes, "codes", I8, (m, w.k_in)), _arg(scale, "scale", F32, (m,), dev), m,
+         _arg(w.codes, "w.codes", I8, (w.n_out, w.k_in), dev), _arg(w.scale, "w.scale", F32, (w.n_out,), dev),
+         w.n_out, w.k_in, _arg(y, "y", BF16, (m, w.n_out), dev))
+    return y

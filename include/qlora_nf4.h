@@ -350,6 +350,97 @@ qn_status qlora_adamw8_step(float* param, const float* grad, int64_t n,
                             void* param_bf16, float lr, float beta1, float beta2, float eps,
                             float weight_decay, int64_t step, qn_stream_t stream);
 
+/* qlora_adamw8_step with the gradient multiplied by *grad_scale (one fp32
+ * value in DEVICE memory, 4-byte aligned; NULL: 1) as it is read: the
+ * clipping coefficient of qlora_grad_norm, with no pass over the gradients
+ * of its own.  The product is rounded to fp32 before the step. */
+qn_status qlora_adamw8_step_scaled(float* param, const float* grad, const float* grad_scale, int64_t n,
+                                   uint8_t* m_codes, float* m_scale, uint8_t* v_codes, float* v_scale,
+                                   void* param_bf16, float lr, float beta1, float beta2, float eps,
+                                   float weight_decay, int64_t step, qn_stream_t stream);
+
+/* ---------------------------------------------------------------- gradient norm */
+
+/* A list of DEVICE tensors (all on the current device).  The arrays are HOST
+ * memory, read during the call only. */
+typedef enum { QN_F32 = 0, QN_BF16 = 1 } qn_dtype;
+typedef struct {
+  int count;                  /* tensors, >= 0                              */
+  const void* const* data;    /* [count]; aligned to the element (not 16 B) */
+  const int64_t* n;           /* [count] values, >= 0 (NULL data allowed at 0) */
+  const int* dtype;           /* [count] qn_dtype                           */
+} qn_tensor_list;
+
+/* The norm of all gradients taken as one vector, and the factor that clips
+ * it to max_norm:
+ *   *norm = sqrt(sum g^2),   *coef = min(1, max_norm / (*norm + 1e-6)).
+ * Squares and sums are fp64 (no overflow below 1e154, fixed order: equal
+ * inputs give equal bits); the norm is rounded once to fp32.  A non-finite
+ * gradient gives a non-finite norm; a NaN norm gives a NaN coef, an infinite
+ * one 0.  norm, coef: fp32 in DEVICE memory (coef may be NULL; max_norm is
+ * then ignored, else it is finite and >= 0).  An empty list has norm 0.
+ * ws: at least qlora_grad_norm_workspace_bytes(count) bytes. */
+size_t qlora_grad_norm_workspace_bytes(int count);
+qn_status qlora_grad_norm(const qn_tensor_list* grads, float max_norm, float* norm, float* coef,
+                          void* ws, size_t ws_bytes, qn_stream_t stream);
+
+/* out[i] = grads[i] * *coef, rounded once to the tensor's type, for callers
+ * whose optimizer does not take the factor itself.  out: NULL (in place;
+ * nothing is written when *coef is 1) or a list of tensors of the same sizes
+ * and types, each either the gradient itself or disjoint from all of them. */
+qn_status qlora_grad_clip(const qn_tensor_list* grads, const qn_tensor_list* out, const float* coef,
+                          qn_stream_t stream);
+
+/* ---------------------------------------------------------------- RMS norm */
+
+/* The norm in front of a block's linears, with the residual addition:
+ *   h = bf16(x + residual)  (h = x without a residual),
+ *   rstd = 1 / sqrt(mean(h^2) + eps),   y = bf16(h * rstd * weight),
+ * row by row, statistics in fp32.  x, residual, h, y bf16 [m, d]; weight
+ * bf16 [d]; d % 8 == 0, d <= 32768 (QN_ERR_SHAPE otherwise); eps >= 0.
+ * residual NULL: h is not written (may be NULL).  h may be x or residual, y
+ * may be x when h is another tensor or not written.
+ * rstd: NULL, or fp32 [m] for the backward. */
+qn_status rmsnorm_fwd(const void* x, const void* residual, const void* weight, int64_t m, int64_t d, float eps,
+                      void* h, void* y, float* rstd, qn_stream_t stream);
+
+/* The same norm with its output in 8 bits, one scale per row, for
+ * int8_linear_fwd: with t = h * weight (exact in fp32) and amax = max |t| of
+ * the row, codes = rint(127 t / amax) (the quotient rounded to fp32, ties to
+ * even) and scale = amax * rstd / 127; codes * scale stands for y.
+ * codes int8 [m, d], scale fp32 [m].  A row of zeros gets scale 0 and codes
+ * 0; a row with a non-finite t gets scale NaN and codes 0 (other rows are
+ * not affected).  Other arguments as for rmsnorm_fwd. */
+qn_status rmsnorm_fwd_int8(const void* x, const void* residual, const void* weight, int64_t m, int64_t d, float eps,
+                           void* h, int8_t* codes, float* scale, qn_stream_t stream);
+
+/* Backward of rmsnorm_fwd from its h and rstd, for dy bf16 [m, d] (gradient
+ * of y) and dh NULL or bf16 [m, d] (gradient of h from the residual stream):
+ *   g = dy * weight,  dx = bf16(dh + rstd (g - h rstd^2 mean(g h))),
+ *   dw = sum over rows of dy * h * rstd   (fp32 [d]; skipped if dw NULL).
+ * dx is the gradient of x and of residual alike; it may be dy or dh.
+ * ws: rmsnorm_bwd_workspace_bytes bytes when dw is given (else ignored). */
+size_t rmsnorm_bwd_workspace_bytes(int64_t m, int64_t d);
+qn_status rmsnorm_bwd(const void* dy, const void* h, const void* weight, const float* rstd, const void* dh,
+                      int64_t m, int64_t d, void* dx, float* dw, void* ws, size_t ws_bytes, qn_stream_t stream);
+
+/* ---------------------------------------------------------------- 8-bit linear */
+
+/* Rows to 8 bits with one scale each: amax = max |x| of the row,
+ * codes = rint(127 x / amax) (rounded as in rmsnorm_fwd_int8), scale =
+ * amax / 127.  x bf16 [m, k], codes int8 [m, k], scale fp32 [m]; k as d of
+ * rmsnorm_fwd; zero and non-finite rows as in rmsnorm_fwd_int8.  Quantizes a
+ * weight [n_out, k_in] (one scale per output channel), such as qlora_merge's,
+ * and tokens that no norm precedes. */
+qn_status int8_quantize_rows(const void* x, int64_t m, int64_t k, int8_t* codes, float* scale, qn_stream_t stream);
+
+/* y = bf16(float(sum_k x w) * (x_scale * w_scale)), the sum over 8-bit codes
+ * in exact 32-bit integers: x_codes int8 [m, k] with x_scale fp32 [m],
+ * w_codes int8 [n, k] with w_scale fp32 [n], y bf16 [m, n].
+ * k % 16 == 0, k < 131072, n % 8 == 0 (QN_ERR_SHAPE otherwise). */
+qn_status int8_linear_fwd(const int8_t* x_codes, const float* x_scale, int64_t m, const int8_t* w_codes,
+                          const float* w_scale, int64_t n, int64_t k, void* y, qn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,9 +30,12 @@ Modules: ``nf4`` (levels, encode, double quantization, dequantization,
 packing, bf16 rounding, the worked-example errors), ``linear`` (the forward
 and backward of the frozen linear with its LoRA path, in fp64), ``merge``
 (the adapter folded into the dequantized weight), ``dropout`` (LoRA
-dropout: the Philox4x32-10 keep mask and the layer with it, in fp64) and
+dropout: the Philox4x32-10 keep mask and the layer with it, in fp64),
 ``adamw8`` (the AdamW step on A and B with 8-bit states: the textbook
-AdamW in fp64, the states stored as E4M3 codes with block scales).
+AdamW in fp64, the states stored as E4M3 codes with block scales), and the
+operators around the linear: ``norm`` (RMS norm with the residual addition,
+its backward, rows in 8 bits), ``int8`` (the linear in 8-bit integers) and
+``grads`` (the global gradient norm and clipping).
 """
 
-from . import nf4, linear, merge, dropout, adamw8  # noqa: F401
+from . import nf4, linear, merge, dropout, adamw8, norm, int8, grads  # noqa: F401
