@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <cstdio>
 #include <array>
+#include <atomic>
 #include <cstdlib>
 #include <mutex>
 #include <utility>
@@ -22,6 +23,7 @@
 #include "gemm_tc.cuh"
 #include "gemv.cuh"
 #include "grad_norm.cuh"
+#include "int8_gemm.cuh"
 #include "int8_linear.cuh"
 #include "lora_small.cuh"
 #include "merge.cuh"
@@ -1597,9 +1599,64 @@ qn_status int8_quantize_rows(const void* x, int64_t m, int64_t k, int8_t* codes,
 
 // ====================================================================== 8-bit linear
 
+namespace {
+
+// 8-bit codes, row-major [outer, inner]: boxes of 128 bytes x box_outer rows,
+// 128-byte swizzle, zero fill out of bounds.
+bool tmap_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_outer) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {inner};
+  cuuint32_t box[2] = {128, box_outer};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Raises a kernel's dynamic shared-memory limit, once per device.
+template <typename K>
+bool set_smem_here(K kernel, size_t bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  if (dev < 64 && (done->load() & bit)) return true;
+  if (!set_smem(kernel, bytes)) return false;
+  if (dev < 64) done->fetch_or(bit);
+  return true;
+}
+
+template <int BN>
+cudaError_t run_int8_gemm(const Int8Params& p, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  using Cfg = I8Cfg<BN>;
+  if (!set_smem_here(int8_gemm_kernel<BN>, Cfg::kSmemBytes, &done)) return cudaErrorInvalidValue;
+  CUtensorMap mx, mw, my;
+  if (!tmap_u8(&mx, p.x, p.k, p.m, 128) || !tmap_u8(&mw, p.w, p.k, p.n, BN / 2) ||
+      !tmap_bf16(&my, p.y, p.n, p.m, p.n, 64, 32)) {
+    set_detail("tensor map", 0);
+    return cudaErrorInvalidValue;
+  }
+  Int8GemmParams g = {};
+  g.xs = p.xs;
+  g.ws = p.ws;
+  g.m = p.m;
+  g.n = p.n;
+  g.ksteps = static_cast<int>(ceil_div(p.k, 128));
+  g.m_tiles = static_cast<int>(ceil_div(p.m, kI8BM));
+  g.n_tiles = static_cast<int>(ceil_div(p.n, BN));
+  const int64_t tiles = static_cast<int64_t>(g.m_tiles) * g.n_tiles;
+  const unsigned grid = static_cast<unsigned>(2 * std::min<int64_t>(tiles, sm_count() / 2));
+  return launch(int8_gemm_kernel<BN>, dim3(grid), dim3(kI8Threads), Cfg::kSmemBytes, st, false, mx, mw, my, g);
+}
+
+}  // namespace
+
 extern "C" qn_status int8_linear_fwd(const int8_t* x_codes, const float* x_scale, int64_t m, const int8_t* w_codes,
                                      const float* w_scale, int64_t n, int64_t k, void* y, qn_stream_t stream) {
   clear_detail();
+  // (coordinates and tile counts stay below 2^31)
   if (m < 0 || n <= 0 || n % 8 != 0 || n > (int64_t{1} << 30) || k <= 0 || k % 16 != 0 || k > kInt8MaxK ||
       m > (int64_t{1} << 30))
     return QN_ERR_SHAPE;
@@ -1617,9 +1674,10 @@ extern "C" qn_status int8_linear_fwd(const int8_t* x_codes, const float* x_scale
   p.m = m;
   p.n = n;
   p.k = k;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (m > 16) return to_status(run_int8_gemm<256>(p, st));
   const dim3 grid(static_cast<unsigned>(ceil_div(n, 16)), static_cast<unsigned>(ceil_div(m, 8)));
-  return to_status(launch(int8_vec_kernel, grid, dim3(kInt8VecThreads), 0, reinterpret_cast<cudaStream_t>(stream),
-                          false, p));
+  return to_status(launch(int8_vec_kernel, grid, dim3(kInt8VecThreads), 0, st, false, p));
 }
 
 // ====================================================================== gradient norm

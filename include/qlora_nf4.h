@@ -106,7 +106,7 @@ void nf4_levels(float out[16]);
  * synchronizes the device first).  *flags_out (HOST) receives the OR of the
  * bits set since the last read; 0 means no bounded wait gave up.  Bits: 1 a
  * wait of the tensor-core GEMM, 2 of the decode GEMV, 4 of a rank-r kernel,
- * QN_WAIT_SELFTEST of qn_selftest_bounded_wait. */
+ * 32 of the 8-bit linear, QN_WAIT_SELFTEST of qn_selftest_bounded_wait. */
 qn_status qn_device_error(int* flags_out);
 
 /* Failure-detection self-test: enqueues one warp whose thread 0 waits on a
