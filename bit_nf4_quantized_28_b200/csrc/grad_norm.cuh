@@ -66,6 +66,8 @@ __global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(const __grid_co
   const uint32_t c1 = static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / gridDim.x);
   double s = 0.0;
   int i = c0 < c1 ? list_find(L, c0) : 0;
+  pdl_launch_dependents();
+  pdl_wait_primary();
   for (uint32_t c = c0; c < c1; ++c) {
     while ((L.end[i] & 0x7FFFFFFFu) <= c) ++i;
     const uint32_t first = i ? (L.end[i - 1] & 0x7FFFFFFFu) : 0u;
@@ -115,6 +117,7 @@ __global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(const __grid_co
 __global__ void __launch_bounds__(kNormThreads) grad_norm_finish_kernel(const double* part, int count, float max_norm,
                                                                         float* norm, float* coef) {
   __shared__ double wsum[kNormThreads / 32];
+  pdl_launch_dependents();
   pdl_wait_primary();
   double s = 0.0;
   for (int i = threadIdx.x; i < count; i += kNormThreads) s += part[i];
@@ -141,6 +144,8 @@ struct GradOut {
 __global__ void __launch_bounds__(kNormThreads) grad_clip_kernel(const __grid_constant__ GradList L,
                                                                  const __grid_constant__ GradOut O,
                                                                  const float* coef) {
+  pdl_launch_dependents();
+  pdl_wait_primary();
   const float f = *coef;
   const uint32_t total = L.end[L.count - 1] & 0x7FFFFFFFu;
   const uint32_t c0 = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / gridDim.x);

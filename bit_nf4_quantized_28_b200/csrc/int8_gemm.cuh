@@ -12,8 +12,9 @@
 //               128-byte swizzle); both CTAs' copies complete on the leader's
 //               barrier
 //   warp 1      MMA issuer (one thread, leader CTA only); owner of TMEM
-//   warps 4-7   epilogue: TMEM -> registers -> scales -> bf16 -> shared memory
-//               -> TMA store, each warp its own 32 rows and staging buffers
+//   warps 4-11  epilogue: TMEM -> registers -> scales -> bf16 -> shared memory
+//               -> TMA store; two warps per 32 rows take the 64-column chunks
+//               in turn, each with a staging buffer of its own
 // The accumulators are double-buffered in TMEM (2 x BN columns), so that the
 // epilogue of a tile runs under the next tile's products.  Every wait is
 // bounded (see mbar_wait); rows past m and channels past n are zero-filled on
@@ -27,7 +28,8 @@ namespace qn {
 
 enum : unsigned int { ERR_INT8_WAIT = 32u };   // a wait of the 8-bit GEMM gave up
 
-constexpr int kI8Threads = 256;
+constexpr int kI8Threads = 384;
+constexpr int kI8EpiWarps = 8;
 constexpr int kI8BM = 256;          // tokens of a CTA pair's tile
 
 template <int BN>
@@ -35,11 +37,12 @@ struct I8Cfg {
   static constexpr uint32_t kABytes = 128 * 128;
   static constexpr uint32_t kBBytes = BN / 2 * 128;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes;
-  static constexpr uint32_t kOutBytes = 4 * 2 * 4096;            // 4 warps x 2 buffers of 32 rows x 64 bf16
+  static constexpr uint32_t kOutBytes = kI8EpiWarps * 4096;      // 32 rows x 64 bf16 of each warp
   static constexpr int kStages = (196608 / kStageBytes) > 8 ? 8 : (196608 / kStageBytes);
   static constexpr uint32_t kOutOff = kStages * kStageBytes;
   static constexpr uint32_t kBarOff = kOutOff + kOutBytes;
-  static constexpr uint32_t kSmemBytes = kBarOff + 256 + 1024;   // + barriers + alignment slack
+  static constexpr uint32_t kScaleOff = kBarOff + 256;           // the tile's BN channel scales
+  static constexpr uint32_t kSmemBytes = kScaleOff + BN * 4 + 1024;   // + alignment slack
   static constexpr uint32_t kTmemCols = 2 * BN;
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
   static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols <= 512, "TMEM columns");
@@ -52,6 +55,41 @@ struct Int8GemmParams {
   int ksteps;             // ceil(k / 128)
   int m_tiles, n_tiles;   // of 256 tokens, of BN channels
 };
+
+// Waits for the phase with the given parity (completed in this CTA, or from
+// the other CTA of the pair with kCluster).  Bounded like mbar_wait, but the
+// timer is not read before 64 tries (each of which suspends the thread a
+// while) have failed: that read would stand in the pipeline's way.
+template <bool kCluster>
+__device__ __forceinline__ bool i8_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t addr = smem_u32(bar);
+  unsigned long long t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (kCluster ? mbar_try_wait_cluster(addr, parity) : mbar_try_wait(addr, parity)) return true;
+    if ((it & 63u) == 0u) {
+      if (*abort) return false;
+      const unsigned long long t = global_ns();
+      if (t0 == 0) {
+        t0 = t;
+      } else if (t - t0 > kWaitLimitNs) {
+        atomicOr(&g_error_word, static_cast<unsigned int>(ERR_INT8_WAIT));
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
 
 // A TMA box whose bytes complete on an mbarrier that may be the other CTA's
 // of the pair (`bar`: a shared::cluster address).  No multicast.
@@ -100,7 +138,7 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 // kind::i8: signed 8-bit A and B, both K-major, 32-bit integer D, shape M x N.
 __host__ __device__ constexpr uint32_t idesc_s8_s32(uint32_t m, uint32_t n) {
@@ -150,7 +188,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 8);       // 4 epilogue warps of each CTA
+      mbar_init(&tempty[i], 2 * kI8EpiWarps);       // both CTAs' epilogue warps
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -163,6 +201,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   __syncthreads();
   tc_fence_after();
   cluster_sync_all();               // both CTAs' barriers are set up
+  pdl_launch_dependents();
+  pdl_wait_primary();
   const uint32_t tmem = *tmem_slot;
 
   const int tiles = p.m_tiles * p.n_tiles;
@@ -170,102 +210,134 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      int it = 0;
+      const uint32_t full0 = map_to_rank(smem_u32(full), 0);
+      int stage = 0, used = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int t = cid; t < tiles && ok; t += ncl) {
         int mt, nt;
         i8_tile(p, t, mt, nt);
         const int row = mt * kI8BM + static_cast<int>(rank) * 128;
         const int col = nt * BN + static_cast<int>(rank) * (BN / 2);
-        for (int ks = 0; ks < p.ksteps; ++ks, ++it) {
-          const int stage = it % S;
-          if (!mbar_wait_cluster(&empty[stage], ((it / S) & 1) ^ 1, abort_flag, ERR_INT8_WAIT)) { ok = false; break; }
+        for (int ks = 0; ks < p.ksteps; ++ks) {
+          if (!i8_wait<true>(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * Cfg::kStageBytes);
-          const uint32_t bar = map_to_rank(smem_u32(&full[stage]), 0);
           uint8_t* sa = smem + stage * Cfg::kStageBytes;
-          tma_load_2d_pair(&tm_x, bar, sa, ks * 128, row);
-          tma_load_2d_pair(&tm_w, bar, sa + Cfg::kABytes, ks * 128, col);
+          tma_load_2d_pair(&tm_x, full0 + 8 * stage, sa, ks * 128, row);
+          tma_load_2d_pair(&tm_w, full0 + 8 * stage, sa + Cfg::kABytes, ks * 128, col);
+          used = max(used, stage + 1);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
       }
-      // the last stages are consumed (so their copies have landed) and their
-      // commits have arrived before this CTA may exit
-      for (int j = (it > S ? it - S : 0); j < it && ok; ++j)
-        ok = mbar_wait_cluster(&empty[j % S], (j / S) & 1, abort_flag, ERR_INT8_WAIT);
+      // the stages' last contents are consumed (so their copies have landed)
+      // and the commits that say so have arrived before this CTA may exit
+      for (int j = 0; j < used && ok; ++j) {
+        if (stage == used) stage = 0, phase ^= 1;
+        ok = i8_wait<true>(&empty[stage], phase ^ 1, abort_flag);
+        ++stage;
+      }
     }
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       constexpr uint32_t idesc = idesc_s8_s32(256, BN);
-      int it = 0, n = 0;
+      // The whole warp runs the loop and one elected lane issues: so the
+      // compiler sees warp-uniform descriptors, which the instruction takes
+      // from uniform registers (issued by a lone thread, each product cost 50
+      // cycles and each commit 100).  Descriptors hold the address in units
+      // of 16 bytes in their low bits.
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(smem), 0, 1024);
+      uint64_t da = desc0;
+      int stage = 0, n = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int t = cid; t < tiles && ok; t += ncl, ++n) {
         const int buf = n & 1;
-        if (!mbar_wait_cluster(&tempty[buf], ((n >> 1) & 1) ^ 1, abort_flag, ERR_INT8_WAIT)) break;
+        if (!__all_sync(0xFFFFFFFFu, i8_wait<true>(&tempty[buf], ((n >> 1) & 1) ^ 1, abort_flag))) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * BN;
-        for (int ks = 0; ks < p.ksteps; ++ks, ++it) {
-          const int stage = it % S;
-          if (!mbar_wait_cluster(&full[stage], (it / S) & 1, abort_flag, ERR_INT8_WAIT)) { ok = false; break; }
+        for (int ks = 0; ks < p.ksteps; ++ks) {
+          if (!__all_sync(0xFFFFFFFFu, i8_wait<true>(&full[stage], phase, abort_flag))) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * Cfg::kStageBytes);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_s8_pair(d, smem_desc_sw128(sa + kk * 32, 0, 1024),
-                         smem_desc_sw128(sa + Cfg::kABytes + kk * 32, 0, 1024), idesc, (ks > 0 || kk > 0) ? 1u : 0u);
-          umma_commit_pair(&empty[stage]);
+            for (int kk = 0; kk < 4; ++kk)
+              umma_s8_pair(d, da + 2 * kk, da + (Cfg::kABytes >> 4) + 2 * kk, idesc, (ks > 0 || kk > 0) ? 1u : 0u);
+            umma_commit_pair(&empty[stage]);
+          }
+          __syncwarp();
+          da += Cfg::kStageBytes >> 4;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+            da = desc0;
+          }
         }
-        if (ok) umma_commit_pair(&tfull[buf]);
+        if (ok && elect_one()) umma_commit_pair(&tfull[buf]);
+        __syncwarp();
       }
     }
   } else if (warp >= 4) {
-    const int wq = warp - 4;
-    uint8_t* const out0 = smem + Cfg::kOutOff + wq * 8192;
-    int n = 0, chunk = 0;
+    const int wq = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t out = smem_u32(smem + Cfg::kOutOff + (warp - 4) * 4096);
+    float* const scales = reinterpret_cast<float*>(smem + Cfg::kScaleOff);
+    const int et = threadIdx.x - 128;
+    int n = 0;
+    bool ok = true;
     for (int t = cid; t < tiles; t += ncl, ++n) {
       const int buf = n & 1;
       int mt, nt;
       i8_tile(p, t, mt, nt);
       const int row0 = mt * kI8BM + static_cast<int>(rank) * 128 + wq * 32;
       const float xs = row0 + lane < p.m ? __ldg(p.xs + row0 + lane) : 0.f;
-      if (!mbar_wait_cluster(&tfull[buf], (n >> 1) & 1, abort_flag, ERR_INT8_WAIT)) break;
+      float ws = 0.f;
+      if (et < BN && static_cast<int64_t>(nt) * BN + et < p.n) ws = __ldg(p.ws + static_cast<int64_t>(nt) * BN + et);
+      named_bar_sync(1, kI8EpiWarps * 32);      // the previous tile's scales have been used
+      if (et < BN) scales[et] = ws;
+      named_bar_sync(1, kI8EpiWarps * 32);
+      // after a wait gave up, go on to the last tile without work: the other
+      // warps may still come to the named barriers
+      ok = ok && __all_sync(0xFFFFFFFFu, i8_wait<true>(&tfull[buf], (n >> 1) & 1, abort_flag));
+      if (!ok) continue;
       tc_fence_after();
       const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(wq * 32) << 16);
+      if (half >= BN / 64 && lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&tempty[buf]), 0));
 #pragma unroll 1
-      for (int c = 0; c < BN / 64; ++c, ++chunk) {
+      for (int c = half; c < BN / 64; c += 2) {
         uint32_t v[2][32];
         tmem_ld32(src + c * 64, v[0]);
         tmem_ld32(src + c * 64 + 32, v[1]);
+        // the staging buffer's last store has read it
+        if (lane == 0) bulk_wait_read0();
         tmem_ld_wait();
-        if (c == BN / 64 - 1) {
+        if (c + 2 >= BN / 64) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&tempty[buf]), 0));
         }
-        // the buffer's store of two chunks ago has read it
-        if (lane == 0) bulk_wait_read1();
         __syncwarp();
-        uint8_t* const out = out0 + (chunk & 1) * 4096;
-        const int64_t col0 = static_cast<int64_t>(nt) * BN + c * 64;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {           // 8 channels at a time
           float f[8];
-          float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
-          if (col0 + 8 * j < p.n) {             // n is a multiple of 8
-            s0 = __ldg(reinterpret_cast<const float4*>(p.ws + col0 + 8 * j));
-            s1 = __ldg(reinterpret_cast<const float4*>(p.ws + col0 + 8 * j) + 1);
-          }
+          const float4 s0 = *reinterpret_cast<const float4*>(scales + c * 64 + 8 * j);
+          const float4 s1 = *reinterpret_cast<const float4*>(scales + c * 64 + 8 * j + 4);
           const float sc[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             f[i] = __int2float_rn(static_cast<int>(v[j >> 2][(j & 3) * 8 + i])) * (xs * sc[i]);
-          const uint32_t a = smem_u32(out) + lane * 128 + ((j ^ (lane & 7)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(pack_bf16x2(f[0], f[1])),
-                       "r"(pack_bf16x2(f[2], f[3])), "r"(pack_bf16x2(f[4], f[5])), "r"(pack_bf16x2(f[6], f[7]))
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                       "r"(pack_bf16x2(f[0], f[1])), "r"(pack_bf16x2(f[2], f[3])), "r"(pack_bf16x2(f[4], f[5])),
+                       "r"(pack_bf16x2(f[6], f[7]))
                        : "memory");
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (col0 < p.n && row0 < p.m) tma_store_2d(&tm_y, out, static_cast<int32_t>(col0), row0);
+          const int64_t col0 = static_cast<int64_t>(nt) * BN + c * 64;
+          if (col0 < p.n && row0 < p.m)
+            tma_store_2d(&tm_y, smem + Cfg::kOutOff + (warp - 4) * 4096, static_cast<int32_t>(col0), row0);
           bulk_commit_group();
         }
       }
@@ -286,6 +358,219 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     }
   }
   if (warp == 1) tmem_dealloc_pair(tmem, Cfg::kTmemCols);
+}
+
+// ====================================================================== few tokens
+//
+// Up to a few hundred tokens the weight's bytes bound the product (one token:
+// 1 byte per two operations), and a grid of output tiles alone has too few
+// CTAs to draw them at HBM's rate.  So the roles are swapped (128 channels
+// are the M of the tensor core's tile, up to 128 tokens its N, padded to 16
+// only) and k is split over the CTAs of a cluster: tiles x splits fill the
+// SMs, and every CTA has its whole ring of TMA copies in flight from the
+// start.  The splits' sums (32-bit integers: exact in any order) are exchanged
+// by bulk copies between the CTAs' shared memories, each CTA finishing its
+// share of the tokens.
+//   warp 0      TMA producer (one lane)
+//   warp 1      MMA issuer (cta_group::1), owner of TMEM
+//   all warps   TMEM -> shared memory -> partners -> sum -> scales -> bf16
+constexpr int kFewThreads = 256;
+constexpr int kFewMaxStages = 12;
+constexpr int kFewTokens = 128;     // of a tile
+
+struct Int8FewParams {
+  const float* xs;
+  const float* ws;
+  __nv_bfloat16* y;
+  int64_t m, n;
+  int ksteps;            // ceil(k / 128)
+  int n_tiles;           // of 128 channels
+  int tok;               // tokens of a tile (the last may have fewer), <= kFewTokens
+  int nt;                // tok rounded up to 16: the instruction's N
+  int splits, stages;
+  uint32_t recv;         // offset of the received sums in shared memory
+  uint32_t tmem_cols;    // power of two >= max(nt, 32)
+};
+
+__device__ __forceinline__ void umma_s8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+__global__ void __launch_bounds__(kFewThreads)
+    int8_few_kernel(const __grid_constant__ CUtensorMap tm_w,    // w codes [n, k], boxes of 128 x 128
+                    const __grid_constant__ CUtensorMap tm_x,    // x codes [m, k], boxes of nt x 128
+                    Int8FewParams p) {
+  extern __shared__ uint8_t few_smem_raw[];
+  __shared__ __align__(8) uint64_t full[kFewMaxStages], empty[kFewMaxStages], done, rx;
+  __shared__ float xs_s[kFewTokens];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(few_smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = p.splits;                     // the cluster's CTAs
+  const int rank = static_cast<int>(blockIdx.x) % splits, tile = static_cast<int>(blockIdx.x) / splits;
+  const int ch0 = (tile % p.n_tiles) * 128;
+  const int64_t t0 = static_cast<int64_t>(tile / p.n_tiles) * p.tok;
+  const int toks = static_cast<int>(min(static_cast<int64_t>(p.tok), p.m - t0));
+  const int k0 = p.ksteps * rank / splits, steps = p.ksteps * (rank + 1) / splits - k0;
+  const uint32_t stage_bytes = 16384u + static_cast<uint32_t>(p.nt) * 128u;
+  const int slice = (toks + splits - 1) / splits;  // tokens that one CTA finishes
+  const int first = rank * slice, mine = max(0, min(slice, toks - first));
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&done, 1);
+    mbar_init(&rx, 1);
+    abort_word = 0;
+    fence_barrier_init();
+    mbar_arrive_expect_tx(&rx, static_cast<uint32_t>((splits - 1) * mine) * 512u);
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_arrive();                                // this CTA's rx barrier is set up
+  const uint32_t tmem = tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait_primary();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t phase = 0;
+      for (int it = 0; it < steps; ++it) {
+        if (!i8_wait<false>(&empty[s], phase ^ 1, abort_flag)) break;
+        uint8_t* dst = ring + s * stage_bytes;
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        tma_load_2d(&tm_w, &full[s], dst, (k0 + it) * 128, ch0);
+        tma_load_2d(&tm_x, &full[s], dst + 16384, (k0 + it) * 128, static_cast<int32_t>(t0));
+        if (++s == p.stages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // (issued by an elected lane of the whole warp: see int8_gemm_kernel)
+    const uint32_t idesc = idesc_s8_s32(128, static_cast<uint32_t>(p.nt));
+    const uint64_t desc0 = smem_desc_sw128(smem_u32(ring), 0, 1024);
+    uint64_t da = desc0;
+    int s = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int it = 0; it < steps; ++it) {
+      if (!__all_sync(0xFFFFFFFFu, i8_wait<false>(&full[s], phase, abort_flag))) { ok = false; break; }
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_s8(tmem, da + 2 * kk, da + 1024 + 2 * kk, idesc, (it > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&empty[s]);
+      }
+      __syncwarp();
+      da += stage_bytes >> 4;
+      if (++s == p.stages) {
+        s = 0;
+        phase ^= 1;
+        da = desc0;
+      }
+    }
+    if (ok && elect_one()) umma_commit(&done);
+    __syncwarp();
+  }
+  // this thread's 8 channels of the final sums
+  const int g8 = (threadIdx.x & 15) * 8;
+  const bool ch_ok = ch0 + g8 < p.n;               // n is a multiple of 8
+  float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
+  if (ch_ok) {
+    s0 = __ldg(reinterpret_cast<const float4*>(p.ws + ch0 + g8));
+    s1 = __ldg(reinterpret_cast<const float4*>(p.ws + ch0 + g8) + 1);
+  }
+  if (threadIdx.x >= 128 && static_cast<int>(threadIdx.x) - 128 < toks)
+    xs_s[threadIdx.x - 128] = __ldg(p.xs + t0 + threadIdx.x - 128);
+  bool have = __all_sync(0xFFFFFFFFu, i8_wait<false>(&done, 0, abort_flag));
+  tc_fence_after();
+  // every product of this CTA is done and the ring is free: the sums go there, [token][channel]
+  int* const stage = reinterpret_cast<int*>(ring);
+  if (have) {
+    const int ch = (warp & 3) * 32 + lane;
+    for (int c = (warp >> 2) * 32; c < toks; c += 64) {
+      uint32_t v[32];
+      tmem_ld32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) stage[(c + j) * 128 + ch] = static_cast<int>(v[j]);
+    }
+  }
+  tc_fence_before();
+  fence_proxy_async_smem();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
+  cluster_wait();                                  // the partners' rx barriers are set up
+  if (splits > 1) {
+    if (have && warp == 0 && lane < splits && lane != rank) {
+      const int n = max(0, min(slice, toks - lane * slice));
+      // slot of this CTA among the receiver's partners
+      const int slot = rank < lane ? rank : rank - 1;
+      if (n > 0)
+        bulk_copy_s2cluster(map_to_rank(smem_u32(ring) + p.recv + static_cast<uint32_t>(slot * n) * 512u, lane),
+                            smem_u32(stage + lane * slice * 128), static_cast<uint32_t>(n) * 512u,
+                            map_to_rank(smem_u32(&rx), lane));
+    }
+    __syncwarp();
+    have = __all_sync(0xFFFFFFFFu, i8_wait<true>(&rx, 0, abort_flag)) && have;
+    cluster_arrive();                              // what the partners sent here has been read
+  }
+  const int* const got = reinterpret_cast<const int*>(ring + p.recv);
+  if (!have) {                                     // copies in flight are given time to land
+    const unsigned long long w0 = global_ns();
+    while (global_ns() - w0 < 100000ull) {
+    }
+  }
+#pragma unroll 4
+  for (int i = threadIdx.x >> 4; i < (have ? mine : 0); i += kFewThreads / 16) {
+    const int4* src = reinterpret_cast<const int4*>(stage + (first + i) * 128 + g8);
+    int4 a = src[0], b = src[1];
+    for (int s = 0; s < splits - 1; ++s) {
+      src = reinterpret_cast<const int4*>(got + (s * mine + i) * 128 + g8);
+      const int4 u = src[0], w = src[1];
+      a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
+      b.x += w.x; b.y += w.y; b.z += w.z; b.w += w.w;
+    }
+    const int64_t row = t0 + first + i;
+    const float x = xs_s[first + i];
+    uint4 o;
+    o.x = pack_bf16x2(__int2float_rn(a.x) * (x * s0.x), __int2float_rn(a.y) * (x * s0.y));
+    o.y = pack_bf16x2(__int2float_rn(a.z) * (x * s0.z), __int2float_rn(a.w) * (x * s0.w));
+    o.z = pack_bf16x2(__int2float_rn(b.x) * (x * s1.x), __int2float_rn(b.y) * (x * s1.y));
+    o.w = pack_bf16x2(__int2float_rn(b.z) * (x * s1.z), __int2float_rn(b.w) * (x * s1.w));
+    if (ch_ok) *reinterpret_cast<uint4*>(p.y + row * p.n + ch0 + g8) = o;
+  }
+  __syncwarp();
+  if (splits > 1) cluster_wait();                  // no CTA leaves before its copies have been read
 }
 
 }  // namespace qn

@@ -30,45 +30,68 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-constexpr int kInt8VecThreads = 256;
+constexpr int kInt8VecTokens = 8;
+constexpr int kInt8VecUnroll = 4;
 
-// 16 output channels x 8 tokens per CTA; its 8 warps take the 64-wide steps
-// of k in turn and add their sums in shared memory.  The weight rows are the
-// A operand (two 16-byte loads per thread and step: 64 contiguous bytes of
-// each of 16 rows), the tokens the B operand.  Within a step the order of k
-// is permuted, alike for both operands, so that a thread's 16 bytes serve as
-// its fragments as they are.
-__global__ void __launch_bounds__(kInt8VecThreads) int8_vec_kernel(Int8Params p) {
-  __shared__ int acc[8][16][8];
+// A few generated tokens: the weight is read once and HBM bounds the product.
+// 16 output channels x up to 8 tokens per CTA; its W warps take the 64-wide
+// steps of k in turn and add their sums in shared memory.  The weight rows
+// are the A operand (two 16-byte loads per thread and step: 64 contiguous
+// bytes of each of 16 rows), the tokens the B operand.  Within a step the
+// order of k is permuted, alike for both operands, so that a thread's 16
+// bytes serve as its fragments as they are: the weight goes from memory to
+// registers to the product, four steps (128 bytes) in flight per thread.
+//
+// W = 8 (two CTAs per SM) while the CTAs fit two per SM, else W = 4 (five per
+// SM), whose 740 slots take the 688 CTAs of 11008 channels at once.  Measured
+// (one token): 11008 x 4096 9.4 us with W = 4, 10.6 with W = 8; 4096 x 11008
+// 9.7 with W = 8, 13.7 with W = 4; two steps in flight 17.6.  (A ring of
+// asynchronous copies in shared memory, 4 to 12 steps deep, over persistent
+// CTAs measured 10.2 to 12.2 and 10.5 to 11.5.)
+template <int W>
+__global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 5) int8_vec_kernel(Int8Params p) {
+  constexpr int U = kInt8VecUnroll;
+  __shared__ int acc[W][16][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16, t0 = static_cast<int64_t>(blockIdx.y) * 8;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
   const int8_t* w0 = p.w + min(n0 + g, p.n - 1) * p.k;
   const int8_t* w1 = p.w + min(n0 + g + 8, p.n - 1) * p.k;
-  const int8_t* xr = p.x + min(t0 + g, p.m - 1) * p.k;
+  const int8_t* xr = p.x + g * p.k;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   int d[4] = {0, 0, 0, 0};
-  for (int64_t k = warp * 64 + q * 16; k - q * 16 < p.k; k += 512) {
-    const bool in = k < p.k;
-    const uint4 a = in ? *reinterpret_cast<const uint4*>(w0 + k) : zero;
-    const uint4 b = in ? *reinterpret_cast<const uint4*>(w1 + k) : zero;
-    const uint4 x = in ? *reinterpret_cast<const uint4*>(xr + k) : zero;
-    const uint32_t f0[4] = {a.x, b.x, a.y, b.y}, f1[4] = {a.z, b.z, a.w, b.w};
-    mma_s8(d, f0, x.x, x.y);
-    mma_s8(d, f1, x.z, x.w);
+  const int kend = static_cast<int>(p.k);
+  const bool tok = g < static_cast<int>(p.m);
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  for (int k = warp * 64 + q * 16; k - q * 16 < kend; k += 64 * W * U) {
+    uint4 a[U], b[U], x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int ku = k + 64 * W * u;
+      const bool in = ku < kend;
+      a[u] = in ? __ldg(reinterpret_cast<const uint4*>(w0 + ku)) : zero;
+      b[u] = in ? __ldg(reinterpret_cast<const uint4*>(w1 + ku)) : zero;
+      x[u] = in && tok ? __ldg(reinterpret_cast<const uint4*>(xr + ku)) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t f0[4] = {a[u].x, b[u].x, a[u].y, b[u].y}, f1[4] = {a[u].z, b[u].z, a[u].w, b[u].w};
+      mma_s8(d, f0, x[u].x, x[u].y);
+      mma_s8(d, f1, x[u].z, x[u].w);
+    }
   }
   acc[warp][g][2 * q] = d[0];
   acc[warp][g][2 * q + 1] = d[1];
   acc[warp][g + 8][2 * q] = d[2];
   acc[warp][g + 8][2 * q + 1] = d[3];
   __syncthreads();
-  if (threadIdx.x < 128) {
-    const int r = threadIdx.x & 15, c = threadIdx.x >> 4;
+  const int r = threadIdx.x & 15, c = threadIdx.x >> 4;
+  if (c < static_cast<int>(p.m) && n0 + r < p.n) {
     int s = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += acc[i][r][c];
-    if (n0 + r < p.n && t0 + c < p.m)
-      p.y[(t0 + c) * p.n + n0 + r] = __float2bfloat16_rn(__int2float_rn(s) * (p.xs[t0 + c] * p.ws[n0 + r]));
+    for (int i = 0; i < W; ++i) s += acc[i][r][c];
+    p.y[c * p.n + n0 + r] = __float2bfloat16_rn(__int2float_rn(s) * (p.xs[c] * p.ws[n0 + r]));
   }
 }
 

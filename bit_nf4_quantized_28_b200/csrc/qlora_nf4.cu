@@ -1460,7 +1460,7 @@ cudaError_t run_rows(const RowParams& p, cudaStream_t st) {
                           : nv == 4 ? row_kernel<4, kRes, kNorm, kInt8>
                                     : row_kernel<8, kRes, kNorm, kInt8>;
   const int64_t grid = std::min<int64_t>(p.m, int64_t{1} << 30);
-  return launch(fn, dim3(static_cast<unsigned>(grid)), dim3(row_threads(p.d, nv)), 0, st, false, p);
+  return launch(fn, dim3(static_cast<unsigned>(grid)), dim3(row_threads(p.d, nv)), 0, st, true, p);
 }
 
 qn_status check_rows(int64_t m, int64_t d) {
@@ -1569,14 +1569,14 @@ qn_status rmsnorm_bwd(const void* dy, const void* h, const void* weight, const f
                                : nv == 4 ? row_bwd_kernel<4, false>
                                          : row_bwd_kernel<8, false>;
     const int64_t grid = std::min<int64_t>(m, int64_t{1} << 30);
-    return to_status(launch(fn, dim3(static_cast<unsigned>(grid)), block, 0, st, false, p));
+    return to_status(launch(fn, dim3(static_cast<unsigned>(grid)), block, 0, st, true, p));
   }
   void (*fn)(RowBwdParams) = nv == 1   ? row_bwd_kernel<1, true>
                              : nv == 2 ? row_bwd_kernel<2, true>
                              : nv == 4 ? row_bwd_kernel<4, true>
                                        : row_bwd_kernel<8, true>;
   const int64_t grid = row_bwd_grid(m);
-  cudaError_t e = launch(fn, dim3(static_cast<unsigned>(grid)), block, 0, st, false, p);
+  cudaError_t e = launch(fn, dim3(static_cast<unsigned>(grid)), block, 0, st, true, p);
   if (e != cudaSuccess) return to_status(e);
   return to_status(launch(row_dw_kernel, dim3(static_cast<unsigned>(ceil_div(d, 32))), dim3(256), 0, st, true,
                           static_cast<const float*>(p.part), dw, static_cast<int>(grid), static_cast<int>(d)));
@@ -1627,6 +1627,58 @@ bool set_smem_here(K kernel, size_t bytes, std::atomic<uint64_t>* done) {
   return true;
 }
 
+// Up to 8 tokens: 16 channels per CTA.
+cudaError_t run_int8_vec(const Int8Params& p, cudaStream_t st) {
+  const int64_t grid = ceil_div(p.n, 16);
+  const bool wide = grid <= 2 * static_cast<int64_t>(sm_count());
+  return launch(wide ? int8_vec_kernel<8> : int8_vec_kernel<4>, dim3(static_cast<unsigned>(grid)),
+                dim3(wide ? 256 : 128), 0, st, true, p);
+}
+
+// Few tokens: 128-channel tiles, k split over a cluster.
+cudaError_t run_int8_few(const Int8Params& p, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  constexpr size_t kFewSmem = 232448 - 1024;     // (1 KB for the static part)
+  if (!set_smem_here(int8_few_kernel, kFewSmem, &done)) return cudaErrorInvalidValue;
+  Int8FewParams f = {};
+  f.xs = p.xs;
+  f.ws = p.ws;
+  f.y = p.y;
+  f.m = p.m;
+  f.n = p.n;
+  f.ksteps = static_cast<int>(ceil_div(p.k, 128));
+  f.n_tiles = static_cast<int>(ceil_div(p.n, 128));
+  const int64_t t_tiles = ceil_div(p.m, kFewTokens);
+  f.tok = static_cast<int>(ceil_div(p.m, t_tiles));
+  f.nt = static_cast<int>(round_up(f.tok, 16));
+  f.tmem_cols = 32;
+  while (f.tmem_cols < static_cast<uint32_t>(f.nt)) f.tmem_cols *= 2;
+  const int64_t tiles = t_tiles * f.n_tiles;
+  f.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sm_count() / tiles, 8, f.ksteps})));
+  // Shared memory: the ring (later the sums of this CTA) and what the
+  // partners send.  One CTA per SM, or two where there are more CTAs than SMs.
+  const size_t stage = 16384 + static_cast<size_t>(f.nt) * 128;
+  const size_t sums = static_cast<size_t>(round_up(f.tok, 32)) * 512;
+  const size_t recv = static_cast<size_t>(f.splits - 1) * ceil_div(f.tok, f.splits) * 512;
+  const size_t room = (tiles * f.splits > sm_count() ? 113 * 1024 : kFewSmem) - 1024 - recv;
+  f.stages = static_cast<int>(std::min<size_t>({room / stage, static_cast<size_t>(kFewMaxStages),
+                                                static_cast<size_t>(ceil_div(f.ksteps, f.splits))}));
+  f.stages = std::max(1, f.stages);
+  f.recv = static_cast<uint32_t>(std::max(stage * f.stages, sums));
+  // at least the share of the SM's shared memory (228 KB, 1 KB of it reserved
+  // per CTA) that tmem_cols is of its 512 TMEM columns: then CTAs that fit an
+  // SM together also fit its TMEM, and no CTA of a cluster ever waits for
+  // columns held by another cluster that waits for it in turn
+  const size_t smem = std::max(f.recv + recv + 1024, static_cast<size_t>(f.tmem_cols) * 456 - 1024);
+  CUtensorMap mw, mx;
+  if (!tmap_u8(&mw, p.w, p.k, p.n, 128) || !tmap_u8(&mx, p.x, p.k, p.m, f.nt)) {
+    set_detail("tensor map", 0);
+    return cudaErrorInvalidValue;
+  }
+  return launch_ex(int8_few_kernel, dim3(static_cast<unsigned>(tiles * f.splits)), dim3(kFewThreads), smem, st, true,
+                   f.splits, mw, mx, f);
+}
+
 template <int BN>
 cudaError_t run_int8_gemm(const Int8Params& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
@@ -1648,7 +1700,7 @@ cudaError_t run_int8_gemm(const Int8Params& p, cudaStream_t st) {
   g.n_tiles = static_cast<int>(ceil_div(p.n, BN));
   const int64_t tiles = static_cast<int64_t>(g.m_tiles) * g.n_tiles;
   const unsigned grid = static_cast<unsigned>(2 * std::min<int64_t>(tiles, sm_count() / 2));
-  return launch(int8_gemm_kernel<BN>, dim3(grid), dim3(kI8Threads), Cfg::kSmemBytes, st, false, mx, mw, my, g);
+  return launch(int8_gemm_kernel<BN>, dim3(grid), dim3(kI8Threads), Cfg::kSmemBytes, st, true, mx, mw, my, g);
 }
 
 }  // namespace
@@ -1675,9 +1727,16 @@ extern "C" qn_status int8_linear_fwd(const int8_t* x_codes, const float* x_scale
   p.n = n;
   p.k = k;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (m > 16) return to_status(run_int8_gemm<256>(p, st));
-  const dim3 grid(static_cast<unsigned>(ceil_div(n, 16)), static_cast<unsigned>(ceil_div(m, 8)));
-  return to_status(launch(int8_vec_kernel, grid, dim3(kInt8VecThreads), 0, st, false, p));
+  if (m <= kInt8VecTokens) return to_status(run_int8_vec(p, st));
+  // One wave of 128 x 128 tiles (k split where they are fewer) while they fit
+  // it, else pairs of CTAs: the figures stand at the kernels.
+  const int64_t sms = sm_count();
+  if (m <= kFewTokens || ceil_div(m, kFewTokens) * ceil_div(n, 128) <= sms) return to_status(run_int8_few(p, st));
+  // A tile of 128 channels takes 0.8 of the time of one of 256 (both are
+  // bound by the operands' way into the SM): taken where that saves waves.
+  const int64_t m_tiles = ceil_div(m, kI8BM);
+  const int64_t w128 = ceil_div(m_tiles * ceil_div(n, 128), sms / 2), w256 = ceil_div(m_tiles * ceil_div(n, 256), sms / 2);
+  return to_status(4 * w128 < 5 * w256 ? run_int8_gemm<128>(p, st) : run_int8_gemm<256>(p, st));
 }
 
 // ====================================================================== gradient norm
@@ -1754,11 +1813,11 @@ qn_status qlora_grad_norm(const qn_tensor_list* grads, float max_norm, float* no
   while (const int64_t chunks = fill_list(grads, nullptr, &at, &g, nullptr)) {
     const int64_t grid = list_grid(chunks);
     const cudaError_t e = launch(grad_norm_kernel, dim3(static_cast<unsigned>(grid)), dim3(kNormThreads), 0, st,
-                                 false, g, part + count);
+                                 true, g, part + count);
     if (e != cudaSuccess) return to_status(e);
     count += static_cast<int>(grid);
   }
-  return to_status(launch(grad_norm_finish_kernel, dim3(1), dim3(kNormThreads), 0, st, count > 0,
+  return to_status(launch(grad_norm_finish_kernel, dim3(1), dim3(kNormThreads), 0, st, true,
                           static_cast<const double*>(part), count, max_norm, norm, coef));
 }
 
@@ -1780,7 +1839,7 @@ qn_status qlora_grad_clip(const qn_tensor_list* grads, const qn_tensor_list* out
   GradOut o;
   while (const int64_t chunks = fill_list(grads, out, &at, &g, &o)) {
     const cudaError_t e = launch(grad_clip_kernel, dim3(static_cast<unsigned>(list_grid(chunks))), dim3(kNormThreads),
-                                 0, reinterpret_cast<cudaStream_t>(stream), false, g, o, coef);
+                                 0, reinterpret_cast<cudaStream_t>(stream), true, g, o, coef);
     if (e != cudaSuccess) return to_status(e);
   }
   return QN_OK;

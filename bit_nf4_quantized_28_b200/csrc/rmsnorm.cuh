@@ -115,6 +115,8 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_kernel(RowParams p) {
   const int nvec = p.d >> 3;
   const int T = blockDim.x, nw = T >> 5;
   int par = 0;
+  pdl_launch_dependents();
+  pdl_wait_primary();
   for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x, par ^= 1) {
     const int64_t base = row * p.d;
     uint4 hv[NV];
@@ -224,6 +226,8 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_bwd_kernel(RowBwdPara
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
   int par = 0;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  pdl_launch_dependents();
+  pdl_wait_primary();
   for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x, par ^= 1) {
     const int64_t base = row * p.d;
     uint4 dyv[NV], hv[NV], av[NV];
@@ -284,6 +288,7 @@ __global__ void __launch_bounds__(256) row_dw_kernel(const float* part, float* d
   __shared__ float acc[8][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  pdl_launch_dependents();
   pdl_wait_primary();
   float s = 0.f;
   if (c < d)
