@@ -21,6 +21,7 @@
 // load and clipped on store by TMA.
 #pragma once
 
+#include "bounded_wait.cuh"
 #include "common.cuh"
 #include "int8_linear.cuh"
 
@@ -55,30 +56,6 @@ struct Int8GemmParams {
   int ksteps;             // ceil(k / 128)
   int m_tiles, n_tiles;   // of 256 tokens, of BN channels
 };
-
-// Waits for the phase with the given parity (completed in this CTA, or from
-// the other CTA of the pair with kCluster).  Bounded like mbar_wait, but the
-// timer is not read before 64 tries (each of which suspends the thread a
-// while) have failed: that read would stand in the pipeline's way.
-template <bool kCluster>
-__device__ __forceinline__ bool i8_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const uint32_t addr = smem_u32(bar);
-  unsigned long long t0 = 0;
-  for (uint32_t it = 1;; ++it) {
-    if (kCluster ? mbar_try_wait_cluster(addr, parity) : mbar_try_wait(addr, parity)) return true;
-    if ((it & 63u) == 0u) {
-      if (*abort) return false;
-      const unsigned long long t = global_ns();
-      if (t0 == 0) {
-        t0 = t;
-      } else if (t - t0 > kWaitLimitNs) {
-        atomicOr(&g_error_word, static_cast<unsigned int>(ERR_INT8_WAIT));
-        *abort = 1;
-        return false;
-      }
-    }
-  }
-}
 
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
@@ -220,7 +197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
         const int row = mt * kI8BM + static_cast<int>(rank) * 128;
         const int col = nt * BN + static_cast<int>(rank) * (BN / 2);
         for (int ks = 0; ks < p.ksteps; ++ks) {
-          if (!i8_wait<true>(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+          if (!bounded_wait<true>(&empty[stage], phase ^ 1, abort_flag, ERR_INT8_WAIT)) { ok = false; break; }
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * Cfg::kStageBytes);
           uint8_t* sa = smem + stage * Cfg::kStageBytes;
           tma_load_2d_pair(&tm_x, full0 + 8 * stage, sa, ks * 128, row);
@@ -236,7 +213,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       // and the commits that say so have arrived before this CTA may exit
       for (int j = 0; j < used && ok; ++j) {
         if (stage == used) stage = 0, phase ^= 1;
-        ok = i8_wait<true>(&empty[stage], phase ^ 1, abort_flag);
+        ok = bounded_wait<true>(&empty[stage], phase ^ 1, abort_flag, ERR_INT8_WAIT);
         ++stage;
       }
     }
@@ -255,11 +232,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       bool ok = true;
       for (int t = cid; t < tiles && ok; t += ncl, ++n) {
         const int buf = n & 1;
-        if (!__all_sync(0xFFFFFFFFu, i8_wait<true>(&tempty[buf], ((n >> 1) & 1) ^ 1, abort_flag))) break;
+        if (!__all_sync(0xFFFFFFFFu, bounded_wait<true>(&tempty[buf], ((n >> 1) & 1) ^ 1, abort_flag, ERR_INT8_WAIT))) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * BN;
         for (int ks = 0; ks < p.ksteps; ++ks) {
-          if (!__all_sync(0xFFFFFFFFu, i8_wait<true>(&full[stage], phase, abort_flag))) { ok = false; break; }
+          if (!__all_sync(0xFFFFFFFFu, bounded_wait<true>(&full[stage], phase, abort_flag, ERR_INT8_WAIT))) { ok = false; break; }
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -299,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       named_bar_sync(1, kI8EpiWarps * 32);
       // after a wait gave up, go on to the last tile without work: the other
       // warps may still come to the named barriers
-      ok = ok && __all_sync(0xFFFFFFFFu, i8_wait<true>(&tfull[buf], (n >> 1) & 1, abort_flag));
+      ok = ok && __all_sync(0xFFFFFFFFu, bounded_wait<true>(&tfull[buf], (n >> 1) & 1, abort_flag, ERR_INT8_WAIT));
       if (!ok) continue;
       tc_fence_after();
       const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(wq * 32) << 16);
@@ -352,11 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
-  if (*abort_flag) {
-    const unsigned long long t0 = global_ns();
-    while (global_ns() - t0 < 100000ull) {
-    }
-  }
+  if (*abort_flag) abort_grace();
   if (warp == 1) tmem_dealloc_pair(tmem, Cfg::kTmemCols);
 }
 
@@ -460,7 +433,7 @@ __global__ void __launch_bounds__(kFewThreads)
       int s = 0;
       uint32_t phase = 0;
       for (int it = 0; it < steps; ++it) {
-        if (!i8_wait<false>(&empty[s], phase ^ 1, abort_flag)) break;
+        if (!bounded_wait<false>(&empty[s], phase ^ 1, abort_flag, ERR_INT8_WAIT)) break;
         uint8_t* dst = ring + s * stage_bytes;
         mbar_arrive_expect_tx(&full[s], stage_bytes);
         tma_load_2d(&tm_w, &full[s], dst, (k0 + it) * 128, ch0);
@@ -481,7 +454,7 @@ __global__ void __launch_bounds__(kFewThreads)
     uint32_t phase = 0;
     bool ok = true;
     for (int it = 0; it < steps; ++it) {
-      if (!__all_sync(0xFFFFFFFFu, i8_wait<false>(&full[s], phase, abort_flag))) { ok = false; break; }
+      if (!__all_sync(0xFFFFFFFFu, bounded_wait<false>(&full[s], phase, abort_flag, ERR_INT8_WAIT))) { ok = false; break; }
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -510,7 +483,7 @@ __global__ void __launch_bounds__(kFewThreads)
   }
   if (threadIdx.x >= 128 && static_cast<int>(threadIdx.x) - 128 < toks)
     xs_s[threadIdx.x - 128] = __ldg(p.xs + t0 + threadIdx.x - 128);
-  bool have = __all_sync(0xFFFFFFFFu, i8_wait<false>(&done, 0, abort_flag));
+  bool have = __all_sync(0xFFFFFFFFu, bounded_wait<false>(&done, 0, abort_flag, ERR_INT8_WAIT));
   tc_fence_after();
   // every product of this CTA is done and the ring is free: the sums go there, [token][channel]
   int* const stage = reinterpret_cast<int*>(ring);
@@ -541,15 +514,11 @@ __global__ void __launch_bounds__(kFewThreads)
                             map_to_rank(smem_u32(&rx), lane));
     }
     __syncwarp();
-    have = __all_sync(0xFFFFFFFFu, i8_wait<true>(&rx, 0, abort_flag)) && have;
+    have = __all_sync(0xFFFFFFFFu, bounded_wait<true>(&rx, 0, abort_flag, ERR_INT8_WAIT)) && have;
     cluster_arrive();                              // what the partners sent here has been read
   }
   const int* const got = reinterpret_cast<const int*>(ring + p.recv);
-  if (!have) {                                     // copies in flight are given time to land
-    const unsigned long long w0 = global_ns();
-    while (global_ns() - w0 < 100000ull) {
-    }
-  }
+  if (!have) abort_grace();
 #pragma unroll 4
   for (int i = threadIdx.x >> 4; i < (have ? mine : 0); i += kFewThreads / 16) {
     const int4* src = reinterpret_cast<const int4*>(stage + (first + i) * 128 + g8);

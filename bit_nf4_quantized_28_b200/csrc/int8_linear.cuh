@@ -30,6 +30,13 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Two products: a thread's 16 bytes of each of its two weight rows and of its token.
+__device__ __forceinline__ void vec_step(int (&d)[4], const uint4& a, const uint4& b, const uint4& x) {
+  const uint32_t f0[4] = {a.x, b.x, a.y, b.y}, f1[4] = {a.z, b.z, a.w, b.w};
+  mma_s8(d, f0, x.x, x.y);
+  mma_s8(d, f1, x.z, x.w);
+}
+
 constexpr int kInt8VecTokens = 8;
 constexpr int kInt8VecUnroll = 4;
 
@@ -40,14 +47,15 @@ constexpr int kInt8VecUnroll = 4;
 // bytes of each of 16 rows), the tokens the B operand.  Within a step the
 // order of k is permuted, alike for both operands, so that a thread's 16
 // bytes serve as its fragments as they are: the weight goes from memory to
-// registers to the product, four steps (128 bytes) in flight per thread.
+// registers to the product, a group of four steps (128 bytes) in flight per
+// thread, or two groups with W = 8.
 //
 // W = 8 (two CTAs per SM) while the CTAs fit two per SM, else W = 4 (five per
 // SM), whose 740 slots take the 688 CTAs of 11008 channels at once.  Measured
-// (one token): 11008 x 4096 9.4 us with W = 4, 10.6 with W = 8; 4096 x 11008
-// 9.7 with W = 8, 13.7 with W = 4; two steps in flight 17.6.  (A ring of
-// asynchronous copies in shared memory, 4 to 12 steps deep, over persistent
-// CTAs measured 10.2 to 12.2 and 10.5 to 11.5.)
+// (one token): 11008 x 4096 9.5 us with W = 4, 10.8 with W = 8; 4096 x 11008
+// 9.9 with W = 8, 10.8 with one group in flight, 13.7 with W = 4; one step in
+// flight 17.6.  (A ring of asynchronous copies in shared memory, 4 to 12
+// steps deep, over persistent CTAs measured 10.2 to 12.2 and 10.5 to 11.5.)
 template <int W>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 5) int8_vec_kernel(Int8Params p) {
   constexpr int U = kInt8VecUnroll;
@@ -64,21 +72,50 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 5) int8_vec_kernel(Int8Pa
   const bool tok = g < static_cast<int>(p.m);
   pdl_launch_dependents();
   pdl_wait_primary();
-  for (int k = warp * 64 + q * 16; k - q * 16 < kend; k += 64 * W * U) {
+  struct Group {
     uint4 a[U], b[U], x[U];
+  };
+  auto fetch = [&](Group& f, int k) {
+    if (k + 64 * W * (U - 1) + 64 <= kend) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int ku = k + 64 * W * u;
-      const bool in = ku < kend;
-      a[u] = in ? __ldg(reinterpret_cast<const uint4*>(w0 + ku)) : zero;
-      b[u] = in ? __ldg(reinterpret_cast<const uint4*>(w1 + ku)) : zero;
-      x[u] = in && tok ? __ldg(reinterpret_cast<const uint4*>(xr + ku)) : zero;
+      for (int u = 0; u < U; ++u) {
+        const int ku = k + 64 * W * u + q * 16;
+        f.a[u] = __ldg(reinterpret_cast<const uint4*>(w0 + ku));
+        f.b[u] = __ldg(reinterpret_cast<const uint4*>(w1 + ku));
+        f.x[u] = tok ? __ldg(reinterpret_cast<const uint4*>(xr + ku)) : zero;
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int ku = k + 64 * W * u + q * 16;
+        const bool in = ku < kend;
+        f.a[u] = in ? __ldg(reinterpret_cast<const uint4*>(w0 + ku)) : zero;
+        f.b[u] = in ? __ldg(reinterpret_cast<const uint4*>(w1 + ku)) : zero;
+        f.x[u] = in && tok ? __ldg(reinterpret_cast<const uint4*>(xr + ku)) : zero;
+      }
     }
+  };
+  auto use = [&](const Group& f) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t f0[4] = {a[u].x, b[u].x, a[u].y, b[u].y}, f1[4] = {a[u].z, b[u].z, a[u].w, b[u].w};
-      mma_s8(d, f0, x[u].x, x[u].y);
-      mma_s8(d, f1, x[u].z, x[u].w);
+    for (int u = 0; u < U; ++u) vec_step(d, f.a[u], f.b[u], f.x[u]);
+  };
+  constexpr int kStep = 64 * W * U;
+  if constexpr (W == 8) {                          // few CTAs: the next group is loaded before this one is used
+    Group f0, f1;
+    fetch(f0, warp * 64);
+    for (int k = warp * 64; k < kend; k += 2 * kStep) {
+      if (k + kStep < kend) fetch(f1, k + kStep);
+      use(f0);
+      if (k + kStep < kend) {
+        if (k + 2 * kStep < kend) fetch(f0, k + 2 * kStep);
+        use(f1);
+      }
+    }
+  } else {
+    for (int k = warp * 64; k < kend; k += kStep) {
+      Group f;
+      fetch(f, k);
+      use(f);
     }
   }
   acc[warp][g][2 * q] = d[0];

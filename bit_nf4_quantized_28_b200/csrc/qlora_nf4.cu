@@ -1433,34 +1433,48 @@ extern "C" qn_status nf4_quantize_noalloc(const void* w_bf16, const qn_nf4_weigh
 
 namespace {
 
-template <typename P>
-struct RowLaunch {
-  void (*fn)(P);
-  int threads;
-};
+// Raises a kernel's dynamic shared-memory limit, once per device.
+template <typename K>
+bool set_smem_here(K kernel, size_t bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  if (dev < 64 && (done->load() & bit)) return true;
+  if (!set_smem(kernel, bytes)) return false;
+  if (dev < 64) done->fetch_or(bit);
+  return true;
+}
 
-// Vectors of 8 values per thread: with few rows as few as fit a CTA (a row's
-// latency counts), else enough for CTAs of at most 256 threads, of which
-// several share an SM and cover one another's reductions.
-int row_nv(int64_t m, int64_t d) {
-  const int64_t nvec = d / 8;
-  const bool many = m >= 2 * static_cast<int64_t>(sm_count());
-  for (int nv = 1; nv < kRowMaxNV; nv *= 2)
-    if (ceil_div(nvec, nv) <= (many ? 256 : row_max_threads(nv))) return nv;
-  return kRowMaxNV;
+constexpr int kRowBwdCtas = 4;              // CTAs per SM of the backward with dw, at most
+constexpr size_t kRowRing = 216 * 1024;     // shared memory of an SM for the rows in flight
+// Vectors of 8 values per thread, at most `most` where the row then fits a
+// CTA: as few as keep an SM's share of the rows within its 2048 threads (with
+// few rows a row's latency counts), but CTAs of no more than `least` threads
+// where there are many rows.
+int row_nv(int64_t m, int64_t d, int least, int most) {
+  const int64_t nvec = d / 8, per_sm = ceil_div(m, sm_count());
+  const int64_t want = std::max<int64_t>(least, 2048 / per_sm);
+  int nv = 1;
+  while (nv < most && ceil_div(nvec, nv) > std::min<int64_t>(want, row_max_threads(nv))) nv *= 2;
+  while (ceil_div(nvec, nv) > row_max_threads(nv)) nv *= 2;
+  return nv;
 }
 
 int row_threads(int64_t d, int nv) { return static_cast<int>(round_up(ceil_div(d / 8, nv), 32)); }
 
-template <bool kRes, bool kNorm, bool kInt8>
-cudaError_t run_rows(const RowParams& p, cudaStream_t st) {
-  const int nv = row_nv(p.m, p.d);
-  void (*fn)(RowParams) = nv == 1   ? row_kernel<1, kRes, kNorm, kInt8>
-                          : nv == 2 ? row_kernel<2, kRes, kNorm, kInt8>
-                          : nv == 4 ? row_kernel<4, kRes, kNorm, kInt8>
-                                    : row_kernel<8, kRes, kNorm, kInt8>;
+cudaError_t launch_rows(void (*fn)(RowParams), const RowParams& p, int nv, cudaStream_t st) {
   const int64_t grid = std::min<int64_t>(p.m, int64_t{1} << 30);
   return launch(fn, dim3(static_cast<unsigned>(grid)), dim3(row_threads(p.d, nv)), 0, st, true, p);
+}
+
+template <bool kRes, bool kInt8>
+cudaError_t run_rows(const RowParams& p, cudaStream_t st) {
+  const int nv = row_nv(p.m, p.d, 128, 4);
+  return launch_rows(nv == 1   ? row_kernel<1, kRes, kInt8>
+                     : nv == 2 ? row_kernel<2, kRes, kInt8>
+                     : nv == 4 ? row_kernel<4, kRes, kInt8>
+                               : row_kernel<8, kRes, kInt8>,
+                     p, nv, st);
 }
 
 qn_status check_rows(int64_t m, int64_t d) {
@@ -1469,7 +1483,7 @@ qn_status check_rows(int64_t m, int64_t d) {
 }
 
 // CTAs of the backward when it also sums dw: each leaves one row of partial sums.
-int64_t row_bwd_grid(int64_t m) { return std::min<int64_t>(m, 2 * static_cast<int64_t>(sm_count())); }
+int64_t row_bwd_grid(int64_t m) { return std::min<int64_t>(m, kRowBwdCtas * static_cast<int64_t>(sm_count())); }
 
 qn_status norm_checks(const void* x, const void* residual, const void* weight, int64_t m, int64_t d, float eps,
                       const void* h) {
@@ -1510,7 +1524,7 @@ qn_status rmsnorm_fwd(const void* x, const void* residual, const void* weight, i
   p.y = static_cast<__nv_bfloat16*>(y);
   p.rstd = rstd;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return to_status(residual ? run_rows<true, true, false>(p, st) : run_rows<false, true, false>(p, st));
+  return to_status(residual ? run_rows<true, false>(p, st) : run_rows<false, false>(p, st));
 }
 
 qn_status rmsnorm_fwd_int8(const void* x, const void* residual, const void* weight, int64_t m, int64_t d, float eps,
@@ -1525,7 +1539,7 @@ qn_status rmsnorm_fwd_int8(const void* x, const void* residual, const void* weig
   p.q = codes;
   p.scale = scale;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return to_status(residual ? run_rows<true, true, true>(p, st) : run_rows<false, true, true>(p, st));
+  return to_status(residual ? run_rows<true, true>(p, st) : run_rows<false, true>(p, st));
 }
 
 size_t rmsnorm_bwd_workspace_bytes(int64_t m, int64_t d) {
@@ -1561,24 +1575,34 @@ qn_status rmsnorm_bwd(const void* dy, const void* h, const void* weight, const f
   p.part = static_cast<float*>(ws);
   p.m = m;
   p.d = static_cast<int>(d);
-  const int nv = row_nv(m, d);
-  const dim3 block(row_threads(d, nv));
   if (!dw) {
-    void (*fn)(RowBwdParams) = nv == 1   ? row_bwd_kernel<1, false>
-                               : nv == 2 ? row_bwd_kernel<2, false>
-                               : nv == 4 ? row_bwd_kernel<4, false>
-                                         : row_bwd_kernel<8, false>;
+    // (three rows' registers: few columns per thread)
+    const int nv = row_nv(m, d, 256, 2);
+    void (*fn)(RowBwdParams) = nv == 1   ? row_bwd_kernel<1>
+                               : nv == 2 ? row_bwd_kernel<2>
+                               : nv == 4 ? row_bwd_kernel<4>
+                                         : row_bwd_kernel<8>;
     const int64_t grid = std::min<int64_t>(m, int64_t{1} << 30);
-    return to_status(launch(fn, dim3(static_cast<unsigned>(grid)), block, 0, st, true, p));
+    return to_status(launch(fn, dim3(static_cast<unsigned>(grid)), dim3(row_threads(d, nv)), 0, st, true, p));
   }
-  void (*fn)(RowBwdParams) = nv == 1   ? row_bwd_kernel<1, true>
-                             : nv == 2 ? row_bwd_kernel<2, true>
-                             : nv == 4 ? row_bwd_kernel<4, true>
-                                       : row_bwd_kernel<8, true>;
-  const int64_t grid = row_bwd_grid(m);
-  cudaError_t e = launch(fn, dim3(static_cast<unsigned>(grid)), block, 0, st, true, p);
+  // One vector per thread where 512 threads hold the row, and about 1024
+  // threads per SM: fewer, wider CTAs leave fewer rows of partial sums.
+  int nv = 1;
+  while (ceil_div(d / 8, nv) > (nv == 1 ? 512 : 1024)) nv *= 2;
+  const int threads = row_threads(d, nv);
+  const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(kRowBwdCtas, 1024 / threads));      // per SM
+  const int64_t grid = std::min<int64_t>(m, ctas * sm_count());
+  const size_t stage = static_cast<size_t>(dh ? 6 : 4) * d;
+  const size_t room = kRowRing / std::min<int64_t>(ceil_div(grid, sm_count()), ctas);
+  p.stages = static_cast<int>(std::max<size_t>(
+      1, std::min<size_t>({room / stage, kRowBwdMaxStages, static_cast<size_t>(ceil_div(m, grid))})));
+  static std::atomic<uint64_t> done[3];
+  const int which = nv == 1 ? 0 : nv == 2 ? 1 : 2;
+  void (*const fn)(RowBwdParams) = nv == 1 ? row_bwd_dw_kernel<1> : nv == 2 ? row_bwd_dw_kernel<2> : row_bwd_dw_kernel<4>;
+  if (!set_smem_here(fn, kRowRing, &done[which])) return to_status(cudaErrorInvalidValue);
+  cudaError_t e = launch(fn, dim3(static_cast<unsigned>(grid)), dim3(threads), stage * p.stages, st, true, p);
   if (e != cudaSuccess) return to_status(e);
-  return to_status(launch(row_dw_kernel, dim3(static_cast<unsigned>(ceil_div(d, 32))), dim3(256), 0, st, true,
+  return to_status(launch(row_dw_kernel, dim3(static_cast<unsigned>(ceil_div(d, 32))), dim3(32 * kRowDwWarps), 0, st, true,
                           static_cast<const float*>(p.part), dw, static_cast<int>(grid), static_cast<int>(d)));
 }
 
@@ -1592,7 +1616,12 @@ qn_status int8_quantize_rows(const void* x, int64_t m, int64_t k, int8_t* codes,
   RowParams p = row_params(x, nullptr, nullptr, m, k, 0.f, nullptr);
   p.q = codes;
   p.scale = scale;
-  return to_status(run_rows<false, false, true>(p, reinterpret_cast<cudaStream_t>(stream)));
+  const int nv = row_nv(m, k, 128, 8);
+  return to_status(launch_rows(nv == 1   ? row_quant_kernel<1>
+                               : nv == 2 ? row_quant_kernel<2>
+                               : nv == 4 ? row_quant_kernel<4>
+                                         : row_quant_kernel<8>,
+                               p, nv, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
@@ -1613,18 +1642,6 @@ bool tmap_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, u
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Raises a kernel's dynamic shared-memory limit, once per device.
-template <typename K>
-bool set_smem_here(K kernel, size_t bytes, std::atomic<uint64_t>* done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  const uint64_t bit = uint64_t{1} << (dev & 63);
-  if (dev < 64 && (done->load() & bit)) return true;
-  if (!set_smem(kernel, bytes)) return false;
-  if (dev < 64) done->fetch_or(bit);
-  return true;
 }
 
 // Up to 8 tokens: 16 channels per CTA.

@@ -19,6 +19,7 @@
 // vectors of 8 values (16-byte accesses), thread tid the vectors tid + i T.
 #pragma once
 
+#include "bounded_wait.cuh"
 #include "common.cuh"
 
 namespace qn {
@@ -32,7 +33,7 @@ constexpr int64_t kRowMaxCols = int64_t{8} * kRowMaxNV * row_max_threads(kRowMax
 struct RowParams {
   const __nv_bfloat16* x;
   const __nv_bfloat16* res;   // kRes only
-  const __nv_bfloat16* w;     // kNorm only
+  const __nv_bfloat16* w;     // [d]
   __nv_bfloat16* h;           // kRes only
   __nv_bfloat16* y;           // bf16 output
   float* rstd;                // [m] or null (bf16 output)
@@ -57,6 +58,25 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
+// Eight sums of bf16 values, each rounded once.  (The fp32 sum rounded to bf16
+// is the same value: where the fp32 sum is inexact, one operand is below
+// 2^-16 of the other, and both roundings give the larger.)
+__device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b) {
+  uint4 r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(a.x), "r"(b.x));
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(a.y), "r"(b.y));
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r.z) : "r"(a.z), "r"(b.z));
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r.w) : "r"(a.w), "r"(b.w));
+  return r;
+}
+
+// The larger magnitude, or NaN if either is NaN.
+__device__ __forceinline__ float max_abs(float a, float t) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(t)));
+  return r;
+}
+
 // Sum and unsigned maximum over the CTA, to every thread, with one barrier.
 // `buf` alternates between calls (two sets of 32 slots each), so that a warp
 // may write the next row's values while another still reads this row's.
@@ -77,38 +97,71 @@ __device__ __forceinline__ void block_sum_max(float& s, uint32_t& a, float* fbuf
   a = __reduce_max_sync(0xFFFFFFFFu, a);
 }
 
-// How a row with the given largest magnitude is brought to integers.  pre is
-// a power of two that keeps 127 t and 127 / amax inside fp32's range; exact,
-// so it changes no code.
+// A row of zeros has scale 0 and codes 0; a row with a non-finite value says
+// so in its scale (NaN) and has codes 0.  Outside [2^-60, 2^100], 127 t or
+// 127 / amax could leave fp32's range: such a row is multiplied by a power of
+// two first (mult), which changes no code.
 struct RowScale {
-  float pre;     // t is multiplied by this first
-  float amax;    // pre * amax
-  float inv;     // 127 / (pre * amax)
-  bool fine;     // finite and not zero
+  bool fine;      // finite and not zero
+  float mult;
+  float amax;     // mult * amax
+  float inv;      // 127 / (mult * amax)
 };
 
 __device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
   RowScale s;
-  const float a = __uint_as_float(amax_bits);
+  const float top = __uint_as_float(amax_bits);
   s.fine = amax_bits != 0u && amax_bits < 0x7F800000u;
-  s.pre = a > 0x1p100f ? 0x1p-32f : (a < 0x1p-60f ? 0x1p80f : 1.f);
-  s.amax = s.fine ? a * s.pre : 1.f;
+  s.mult = top > 0x1p100f ? 0x1p-32f : (top < 0x1p-60f ? 0x1p80f : 1.f);
+  s.amax = s.fine ? top * s.mult : 1.f;
   s.inv = __fdiv_rn(127.f, s.amax);
   return s;
 }
 
-// rint(127 t / amax), the quotient rounded to fp32 first (ties to even).
-// t * (127 / amax) is within 127 * 2^-23 < 2^-15 of it, so the division is
-// needed only where that product lies within 2^-14 of a half-integer.
-__device__ __forceinline__ int row_code(float t, const RowScale& s) {
-  t *= s.pre;
-  const float v = t * s.inv;
-  float n = rintf(v);
-  if (fabsf(fabsf(v - n) - 0.5f) < 0x1p-14f) n = rintf(__fdiv_rn(127.f * t, s.amax));
-  return static_cast<int>(n);
+// Codes of 8 values (already multiplied by mult): q = rint(127 t / amax), the
+// quotient rounded to fp32 first (ties to even).  t * inv is within
+// 127 * 2^-24 < 2^-16 of the exact quotient, so the division is needed only
+// where it lies within 2^-14 of a half-integer (one value in 8000): checked
+// once for the 8.  Adding 1.5 * 2^23 rounds to an integer (ties to even)
+// whose low byte is the code.
+__device__ __forceinline__ uint2 row_codes(const float (&t)[8], const RowScale& s) {
+  constexpr float kMagic = 12582912.f;
+  uint32_t c[8];
+  float off = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float n = fmaf(t[j], s.inv, kMagic);
+    off = fmaxf(off, fabsf(fmaf(t[j], s.inv, kMagic - n)));
+    c[j] = __float_as_uint(n);
+  }
+  if (off > 0.5f - 0x1p-14f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = __float_as_uint(__fdiv_rn(127.f * t[j], s.amax) + kMagic);
+  }
+  return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040u), __byte_perm(c[2], c[3], 0x0040u), 0x5410u),
+                    __byte_perm(__byte_perm(c[4], c[5], 0x0040u), __byte_perm(c[6], c[7], 0x0040u), 0x5410u));
 }
 
-template <int NV, bool kRes, bool kNorm, bool kInt8>
+// The codes of a row's vector, stored; t is scaled in place where the row's
+// magnitude asks for it.
+__device__ __forceinline__ void store_codes(int8_t* out, float (&t)[8], const RowScale& s) {
+  uint2 q = make_uint2(0u, 0u);
+  if (s.fine) {
+    if (s.mult != 1.f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] *= s.mult;
+    }
+    q = row_codes(t, s);
+  }
+  *reinterpret_cast<uint2*>(out) = q;
+}
+
+__device__ __forceinline__ float row_scale_value(uint32_t amax_bits, float rstd) {
+  return amax_bits >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
+                                  : __fdiv_rn(__uint_as_float(amax_bits) * rstd, 127.f);
+}
+
+template <int NV, bool kRes, bool kInt8>
 __global__ void __launch_bounds__(row_max_threads(NV)) row_kernel(RowParams p) {
   __shared__ float fbuf[2][32];
   __shared__ uint32_t ubuf[2][32];
@@ -121,7 +174,6 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_kernel(RowParams p) {
     const int64_t base = row * p.d;
     uint4 hv[NV];
     float ssq = 0.f;
-    uint32_t amax = 0u;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * T;
@@ -137,54 +189,39 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_kernel(RowParams p) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = threadIdx.x + i * T;
-        float a[8], b[8];
-        unpack8(hv[i], a);
-        unpack8(rv[i], b);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] += b[j];
-        hv[i] = pack8(a);
+        hv[i] = add8(hv[i], rv[i]);
         if (v < nvec) *reinterpret_cast<uint4*>(p.h + base + 8 * v) = hv[i];
       }
     }
-    float t[NV][8];
+    auto weight = [&](int v) {
+      return v < nvec ? __ldg(reinterpret_cast<const uint4*>(p.w) + v) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    float t[kInt8 ? NV : 1][8];
+    float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = threadIdx.x + i * T;
-      unpack8(hv[i], t[i]);
-      if constexpr (kNorm) {
-        float wf[8];
-        unpack8(v < nvec ? __ldg(reinterpret_cast<const uint4*>(p.w) + v) : make_uint4(0u, 0u, 0u, 0u), wf);
+      float f[8], wf[8];
+      unpack8(hv[i], f);
+      if constexpr (kInt8) unpack8(weight(threadIdx.x + i * T), wf);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          ssq = fmaf(t[i][j], t[i][j], ssq);
-          t[i][j] *= wf[j];
+      for (int j = 0; j < 8; ++j) {
+        ssq = fmaf(f[j], f[j], ssq);
+        if constexpr (kInt8) {
+          t[i][j] = f[j] * wf[j];
+          amax = max_abs(amax, t[i][j]);
         }
       }
-      if constexpr (kInt8) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(t[i][j]) & 0x7FFFFFFFu);
-      }
     }
-    block_sum_max(ssq, amax, fbuf[par], ubuf[par], nw);
-    const float rstd = kNorm ? __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(ssq, static_cast<float>(p.d)) + p.eps)) : 1.f;
+    uint32_t top = __float_as_uint(amax);
+    block_sum_max(ssq, top, fbuf[par], ubuf[par], nw);
+    const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(ssq, static_cast<float>(p.d)) + p.eps));
     if constexpr (kInt8) {
-      const RowScale s = row_scale(amax);
-      if (threadIdx.x == 0) {
-        // a row with a non-finite value: its scale says so (NaN), its codes are 0
-        const float a = __uint_as_float(amax);
-        p.scale[row] = amax >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __fdiv_rn(kNorm ? a * rstd : a, 127.f);
-      }
+      const RowScale s = row_scale(top);
+      if (threadIdx.x == 0) p.scale[row] = row_scale_value(top, rstd);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = threadIdx.x + i * T;
-        if (v >= nvec) continue;
-        uint32_t o[2] = {0u, 0u};
-        if (s.fine) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            o[j >> 2] |= (static_cast<uint32_t>(row_code(t[i][j], s)) & 0xFFu) << (8 * (j & 3));
-        }
-        *reinterpret_cast<uint2*>(p.q + base + 8 * v) = make_uint2(o[0], o[1]);
+        if (v < nvec) store_codes(p.q + base + 8 * v, t[i], s);
       }
     } else {
       if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
@@ -192,13 +229,63 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_kernel(RowParams p) {
       for (int i = 0; i < NV; ++i) {
         const int v = threadIdx.x + i * T;
         if (v >= nvec) continue;
+        float f[8], wf[8];
+        unpack8(hv[i], f);
+        unpack8(weight(v), wf);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t[i][j] *= rstd;
-        *reinterpret_cast<uint4*>(p.y + base + 8 * v) = pack8(t[i]);
+        for (int j = 0; j < 8; ++j) f[j] = f[j] * wf[j] * rstd;
+        *reinterpret_cast<uint4*>(p.y + base + 8 * v) = pack8(f);
       }
     }
   }
 }
+
+// Rows to 8 bits without a norm.  The values stay packed (two to a register)
+// until they are quantized: bf16 magnitudes order as unsigned 16-bit integers,
+// so the row's largest is found two at a time, and few registers let more
+// rows share an SM.
+template <int NV>
+__global__ void __launch_bounds__(row_max_threads(NV)) row_quant_kernel(RowParams p) {
+  __shared__ float fbuf[2][32];
+  __shared__ uint32_t ubuf[2][32];
+  const int nvec = p.d >> 3;
+  const int T = blockDim.x, nw = T >> 5;
+  int par = 0;
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x, par ^= 1) {
+    const int64_t base = row * p.d;
+    uint4 hv[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * T;
+      hv[i] = v < nvec ? *reinterpret_cast<const uint4*>(p.x + base + 8 * v) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    uint32_t two = 0u;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t u[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        asm("max.u16x2 %0, %1, %2;" : "=r"(two) : "r"(two), "r"(u[j] & 0x7FFF7FFFu));
+    }
+    uint32_t amax = max(two << 16, two & 0xFFFF0000u);
+    float none = 0.f;
+    block_sum_max(none, amax, fbuf[par], ubuf[par], nw);
+    const RowScale s = row_scale(amax);
+    if (threadIdx.x == 0) p.scale[row] = row_scale_value(amax, 1.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * T;
+      if (v >= nvec) continue;
+      float f[8];
+      unpack8(hv[i], f);
+      store_codes(p.q + base + 8 * v, f, s);
+    }
+  }
+}
+
+enum : unsigned int { ERR_ROW_WAIT = 64u };   // a wait of the norm's backward gave up
 
 struct RowBwdParams {
   const __nv_bfloat16* dy;
@@ -207,23 +294,19 @@ struct RowBwdParams {
   const float* rstd;
   const __nv_bfloat16* dh;    // or null
   __nv_bfloat16* dx;
-  float* part;                // kDw: [gridDim.x, d]
+  float* part;                // with dw: [gridDim.x, d]
   int64_t m;
   int d;
+  int stages;                 // with dw: rows in flight
 };
 
-template <int NV, bool kDw>
+template <int NV>
 __global__ void __launch_bounds__(row_max_threads(NV)) row_bwd_kernel(RowBwdParams p) {
   __shared__ float fbuf[2][32];
   __shared__ uint32_t ubuf[2][32];
   const int nvec = p.d >> 3;
   const int T = blockDim.x, nw = T >> 5;
   const float inv_d = 1.f / static_cast<float>(p.d);
-  float dw[kDw ? NV : 1][8];
-#pragma unroll
-  for (int i = 0; i < (kDw ? NV : 1); ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
   int par = 0;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   pdl_launch_dependents();
@@ -248,10 +331,7 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_bwd_kernel(RowBwdPara
       unpack8(hv[i], b);
       unpack8(v < nvec ? __ldg(reinterpret_cast<const uint4*>(p.w) + v) : zero, c);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if constexpr (kDw) dw[i][j] = fmaf(a[j], b[j] * rstd, dw[i][j]);
-        dot = fmaf(a[j] * c[j], b[j], dot);
-      }
+      for (int j = 0; j < 8; ++j) dot = fmaf(a[j] * c[j], b[j], dot);
     }
     uint32_t none = 0u;
     block_sum_max(dot, none, fbuf[par], ubuf[par], nw);
@@ -270,35 +350,140 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_bwd_kernel(RowBwdPara
       *reinterpret_cast<uint4*>(p.dx + base + 8 * v) = pack8(a);
     }
   }
-  if constexpr (kDw) {
-    float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.d;
+}
+
+// The backward that also sums dw: a CTA takes many rows and a thread keeps the
+// sums of its columns in registers, which leaves too few of them to hold the
+// next rows' loads.  So rows come through a ring in shared memory (bulk
+// copies of dy, h and dh, `stages` rows deep), and each is read there twice.
+constexpr int kRowBwdMaxStages = 4;
+
+template <int NV>
+__global__ void __launch_bounds__(1024) row_bwd_dw_kernel(RowBwdParams p) {
+  extern __shared__ __align__(128) uint8_t row_ring[];
+  __shared__ __align__(8) uint64_t full[kRowBwdMaxStages];
+  __shared__ float fbuf[2][32];
+  __shared__ uint32_t ubuf[2][32];
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+  const int nvec = p.d >> 3, S = p.stages;
+  const int T = blockDim.x, nw = T >> 5;
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  const uint32_t row_bytes = static_cast<uint32_t>(p.d) * 2u;
+  const uint32_t stage_bytes = (p.dh ? 3u : 2u) * row_bytes;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) mbar_init(&full[i], 1);
+    abort_word = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  auto issue = [&](int64_t row, int stage) {
+    uint8_t* dst = row_ring + stage * stage_bytes;
+    const int64_t base = row * p.d;
+    mbar_arrive_expect_tx(&full[stage], stage_bytes);
+    bulk_copy_g2s(dst, p.dy + base, row_bytes, &full[stage]);
+    bulk_copy_g2s(dst + row_bytes, p.h + base, row_bytes, &full[stage]);
+    if (p.dh) bulk_copy_g2s(dst + 2 * row_bytes, p.dh + base, row_bytes, &full[stage]);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < S; ++i) {
+      const int64_t row = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
+      if (row < p.m) issue(row, i);
+    }
+  float dw[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  int stage = 0, par = 0;
+  uint32_t phase = 0;
+  for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x, par ^= 1) {
+    const float rstd = __ldg(p.rstd + row);
+    // (a wait that gave up leaves its mark in the error word; the rows go on, so that the barriers meet)
+    bounded_wait<false>(&full[stage], phase, abort_flag, ERR_ROW_WAIT);
+    const uint4* sdy = reinterpret_cast<const uint4*>(row_ring + stage * stage_bytes);
+    const uint4* sh = sdy + nvec;
+    const uint4* sdh = sh + nvec;
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * T;
+      float a[8], b[8], c[8];
+      unpack8(v < nvec ? sdy[v] : zero, a);
+      unpack8(v < nvec ? sh[v] : zero, b);
+      unpack8(v < nvec ? __ldg(reinterpret_cast<const uint4*>(p.w) + v) : zero, c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[i][j] = fmaf(a[j], b[j] * rstd, dw[i][j]);
+        dot = fmaf(a[j] * c[j], b[j], dot);
+      }
+    }
+    uint32_t none = 0u;
+    block_sum_max(dot, none, fbuf[par], ubuf[par], nw);
+    // past that barrier every thread is done with the previous row's stage
+    if (threadIdx.x == 0 && S > 1 && row >= gridDim.x) {
+      const int64_t next = row + static_cast<int64_t>(S - 1) * gridDim.x;
+      if (next < p.m) issue(next, stage ? stage - 1 : S - 1);
+    }
+    const float c1 = dot * inv_d * rstd * rstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * T;
       if (v >= nvec) continue;
-      float4* o = reinterpret_cast<float4*>(out + 8 * v);
-      o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-      o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+      float a[8], b[8], c[8], e[8];
+      unpack8(sdy[v], a);
+      unpack8(sh[v], b);
+      unpack8(__ldg(reinterpret_cast<const uint4*>(p.w) + v), c);
+      unpack8(p.dh ? sdh[v] : zero, e);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] = fmaf(rstd, fmaf(-b[j], c1, a[j] * c[j]), e[j]);
+      *reinterpret_cast<uint4*>(p.dx + row * p.d + 8 * v) = pack8(a);
+    }
+    if (S == 1) {
+      __syncthreads();
+      if (threadIdx.x == 0 && row + gridDim.x < p.m) issue(row + gridDim.x, 0);
+    }
+    if (++stage == S) {
+      stage = 0;
+      phase ^= 1;
     }
   }
+  float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.d;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = threadIdx.x + i * T;
+    if (v >= nvec) continue;
+    float4* o = reinterpret_cast<float4*>(out + 8 * v);
+    o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+    o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+  }
+  if (abort_word) abort_grace();
 }
 
-// dw = column sums of the CTAs' partial sums, in a fixed order.
-__global__ void __launch_bounds__(256) row_dw_kernel(const float* part, float* dw, int rows, int d) {
-  __shared__ float acc[8][33];
+// dw = column sums of the CTAs' partial sums, in a fixed order: 16 warps take
+// the rows in turn, 32 columns per CTA, and their sums are added pairwise.
+constexpr int kRowDwWarps = 16;
+
+__global__ void __launch_bounds__(32 * kRowDwWarps) row_dw_kernel(const float* part, float* dw, int rows, int d) {
+  __shared__ float acc[kRowDwWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   pdl_launch_dependents();
   pdl_wait_primary();
   float s = 0.f;
-  if (c < d)
-    for (int r = warp; r < rows; r += 8) s += part[static_cast<int64_t>(r) * d + c];
-  acc[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < d) {
-    for (int i = 1; i < 8; ++i) s += acc[i][lane];
-    dw[c] = s;
+  if (c < d) {
+#pragma unroll 8
+    for (int r = warp; r < rows; r += kRowDwWarps) s += part[static_cast<int64_t>(r) * d + c];
   }
+  acc[warp][lane] = s;
+  for (int n = kRowDwWarps / 2; n > 0; n /= 2) {
+    __syncthreads();
+    if (warp < n) acc[warp][lane] += acc[warp + n][lane];
+  }
+  if (warp == 0 && c < d) dw[c] = acc[0][lane];
 }
 
 }  // namespace qn
