@@ -45,13 +45,39 @@ struct AdamW8Params {
   float b1, omb1, b2, omb2, step_size, rsqrt_bc2, decay, eps;
 };
 
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(c), __NV_E4M3)));
+// Four E4M3 codes (the bytes of a word) -> their values, two at a time.
+__device__ __forceinline__ void e4m3_values(uint32_t w, float* v) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * i)), __NV_E4M3));
+    const float2 f = __half22float2(h);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
 }
 
-__device__ __forceinline__ uint8_t e4m3_code(float x) {
-  const uint8_t c = static_cast<uint8_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3));
-  return (c & 0x7Fu) ? c : uint8_t{0};
+// Four values -> E4M3 codes (nearest, ties to even, saturating), zero as +0.
+__device__ __forceinline__ uint32_t e4m3_codes(const float* x) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t w = lo | (hi << 16);
+  const uint32_t mag = w & 0x7F7F7F7Fu;
+  return mag | (w & (mag + 0x7F7F7F7Fu) & 0x80808080u);      // the sign of the bytes that are not zero
+}
+
+// Codes of 8 values: x * inv, inv = 448 / absmax, or x / scale where that
+// reciprocal overflows.
+__device__ __forceinline__ uint2 adam_codes(const float (&x)[8], float scale, float inv) {
+  float y[8];
+  if (!(scale > 0.f)) return make_uint2(0u, 0u);
+  if (isfinite(inv)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(x[j], inv);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(x[j], scale);
+  }
+  return make_uint2(e4m3_codes(y), e4m3_codes(y + 4));
 }
 
 __global__ void __launch_bounds__(kAdamThreads) adamw8_kernel(AdamW8Params p) {
@@ -65,21 +91,19 @@ __global__ void __launch_bounds__(kAdamThreads) adamw8_kernel(AdamW8Params p) {
     const int64_t e0 = b * kAdamBlock + 8 * lane;
     const bool full = e0 + 8 <= p.n;
     float pv[8], gv[8];
-    uint8_t mcv[8], vcv[8];
+    uint2 mcw = make_uint2(0u, 0u), vcw = mcw;      // the codes of 8 values
     if (full) {
       const float4* ps = reinterpret_cast<const float4*>(p.p + e0);
       const float4* gs = reinterpret_cast<const float4*>(p.g + e0);
       const float4 p0 = ps[0], p1 = ps[1], g0 = gs[0], g1 = gs[1];
-      const uint2 mw = *reinterpret_cast<const uint2*>(p.mc + e0);
-      const uint2 vw = *reinterpret_cast<const uint2*>(p.vc + e0);
+      mcw = *reinterpret_cast<const uint2*>(p.mc + e0);
+      vcw = *reinterpret_cast<const uint2*>(p.vc + e0);
       const float pa[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
       const float ga[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         pv[j] = pa[j];
         gv[j] = ga[j];
-        mcv[j] = static_cast<uint8_t>(((j < 4 ? mw.x : mw.y) >> (8 * (j & 3))) & 0xFFu);
-        vcv[j] = static_cast<uint8_t>(((j < 4 ? vw.x : vw.y) >> (8 * (j & 3))) & 0xFFu);
       }
     } else {
 #pragma unroll
@@ -87,17 +111,22 @@ __global__ void __launch_bounds__(kAdamThreads) adamw8_kernel(AdamW8Params p) {
         const bool ok = e0 + j < p.n;
         pv[j] = ok ? p.p[e0 + j] : 0.f;
         gv[j] = ok ? p.g[e0 + j] : 0.f;
-        mcv[j] = ok ? p.mc[e0 + j] : uint8_t{0};
-        vcv[j] = ok ? p.vc[e0 + j] : uint8_t{0};
+        const uint32_t mb = ok ? p.mc[e0 + j] : 0u, vb = ok ? p.vc[e0 + j] : 0u;
+        (j < 4 ? mcw.x : mcw.y) |= mb << (8 * (j & 3));
+        (j < 4 ? vcw.x : vcw.y) |= vb << (8 * (j & 3));
       }
     }
     const float msc = p.ms[b], vsc = p.vs[b];
     float mn[8], vn[8], pn[8];
+    e4m3_values(mcw.x, mn);
+    e4m3_values(mcw.y, mn + 4);
+    e4m3_values(vcw.x, vn);
+    e4m3_values(vcw.y, vn + 4);
     float am = 0.f, av = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float m0 = __fmul_rn(e4m3_value(mcv[j]), msc);
-      const float v0 = __fmul_rn(e4m3_value(vcv[j]), vsc);
+      const float m0 = __fmul_rn(mn[j], msc);
+      const float v0 = __fmul_rn(vn[j], vsc);
       const float g = __fmul_rn(gv[j], gs);
       mn[j] = __fadd_rn(__fmul_rn(p.b1, m0), __fmul_rn(p.omb1, g));
       vn[j] = __fadd_rn(__fmul_rn(p.b2, v0), __fmul_rn(p.omb2, __fmul_rn(g, g)));
@@ -131,26 +160,16 @@ __global__ void __launch_bounds__(kAdamThreads) adamw8_kernel(AdamW8Params p) {
       av = fmaxf(av, __shfl_xor_sync(0xFFFFFFFFu, av, o));
     }
     const float sm = __fdiv_rn(am, 448.f), sv = __fdiv_rn(av, 448.f);
-    // codes from x * (448 / absmax), or x / scale where that reciprocal overflows
-    const float im = am > 0.f ? __fdiv_rn(448.f, am) : 1.f, iv = av > 0.f ? __fdiv_rn(448.f, av) : 1.f;
-    const bool mfast = isfinite(im), vfast = isfinite(iv);
-    uint32_t mw[2] = {0u, 0u}, vw[2] = {0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t cm = sm > 0.f ? e4m3_code(mfast ? __fmul_rn(mn[j], im) : __fdiv_rn(mn[j], sm)) : 0u;
-      const uint32_t cv = sv > 0.f ? e4m3_code(vfast ? __fmul_rn(vn[j], iv) : __fdiv_rn(vn[j], sv)) : 0u;
-      mw[j >> 2] |= cm << (8 * (j & 3));
-      vw[j >> 2] |= cv << (8 * (j & 3));
-    }
+    const uint2 mw = adam_codes(mn, sm, __fdiv_rn(448.f, am)), vw = adam_codes(vn, sv, __fdiv_rn(448.f, av));
     if (full) {
-      *reinterpret_cast<uint2*>(p.mc + e0) = make_uint2(mw[0], mw[1]);
-      *reinterpret_cast<uint2*>(p.vc + e0) = make_uint2(vw[0], vw[1]);
+      *reinterpret_cast<uint2*>(p.mc + e0) = mw;
+      *reinterpret_cast<uint2*>(p.vc + e0) = vw;
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (e0 + j >= p.n) break;
-        p.mc[e0 + j] = static_cast<uint8_t>((mw[j >> 2] >> (8 * (j & 3))) & 0xFFu);
-        p.vc[e0 + j] = static_cast<uint8_t>((vw[j >> 2] >> (8 * (j & 3))) & 0xFFu);
+        p.mc[e0 + j] = static_cast<uint8_t>(((j < 4 ? mw.x : mw.y) >> (8 * (j & 3))) & 0xFFu);
+        p.vc[e0 + j] = static_cast<uint8_t>(((j < 4 ? vw.x : vw.y) >> (8 * (j & 3))) & 0xFFu);
       }
     }
     if (lane == 0) {

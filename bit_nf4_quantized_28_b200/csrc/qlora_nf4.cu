@@ -1254,7 +1254,7 @@ qn_status qlora_adamw8_step_scaled(float* param, const float* grad, const float*
   const int64_t grid = std::min<int64_t>(ceil_div(nblk, kAdamThreads / 32),
                                          static_cast<int64_t>(std::max(per_sm, 1)) * sm_count());
   return to_status(launch(adamw8_kernel, dim3(static_cast<unsigned>(grid)), dim3(kAdamThreads), 0,
-                          reinterpret_cast<cudaStream_t>(stream), false, a));
+                          reinterpret_cast<cudaStream_t>(stream), true, a));
 }
 
 size_t qlora_dropout_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in, int r) {
