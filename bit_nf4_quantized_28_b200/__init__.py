@@ -128,8 +128,14 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _raw_stream(index):
+    """The current stream of device `index` as an address (without building a
+    torch.cuda.Stream for it: 0.2 instead of 4 us)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
 
 
 def _check(status, what):
@@ -144,25 +150,26 @@ def _arg(t, what, dtype, shape, device=None):
     address (None for None)."""
     if t is None:
         return None
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous {dtype} cuda tensor is needed, got {t.dtype} on {t.device}, "
-                         f"strides {t.stride()}")
+    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous() and (
+            device is None or t.device == device):
+        return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what}: is on {t.device}, the other tensors are on {device}")
-    return t.data_ptr()
+    raise ValueError(f"{what}: a contiguous {dtype} tensor on {device or 'a cuda device'} is needed, got {t.dtype} on "
+                     f"{t.device}, strides {t.stride()}")
 
 
 def _run(name, device, *args):
     """Calls `name` with the current stream of `device` (made current for the call)."""
     fn = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    _check(status, name)
+            status = fn(*args, _raw_stream(index))
+    if status != 0:
+        _check(status, name)
 
 
 def levels():

@@ -1810,7 +1810,7 @@ extern "C" {
 size_t qlora_grad_norm_workspace_bytes(int count) {
   if (count < 0) return 0;
   const int64_t launches = std::max<int64_t>(1, ceil_div(count, kListMax));
-  return align256(static_cast<size_t>(launches) * 8 * sm_count() * sizeof(double));
+  return align256(static_cast<size_t>(launches) * 8 * sm_count() * sizeof(double)) + 256;
 }
 
 qn_status qlora_grad_norm(const qn_tensor_list* grads, float max_norm, float* norm, float* coef, void* ws,
@@ -1824,18 +1824,33 @@ qn_status qlora_grad_norm(const qn_tensor_list* grads, float max_norm, float* no
   if (!aligned16(ws)) return QN_ERR_ALIGN;
   if (!device_is_sm100()) return QN_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  double* part = static_cast<double*>(ws);
-  int count = 0, at = 0;
+  NormOut o = {};
+  o.counter = static_cast<unsigned int*>(ws);
+  o.part = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + 256);
+  o.max_norm = max_norm;
+  o.norm = norm;
+  o.coef = coef;
+  // the call's CTAs are counted before its first launch (one launch takes
+  // kListMax tensors, so that most calls have one)
+  int at = 0;
   GradList g;
-  while (const int64_t chunks = fill_list(grads, nullptr, &at, &g, nullptr)) {
-    const int64_t grid = list_grid(chunks);
-    const cudaError_t e = launch(grad_norm_kernel, dim3(static_cast<unsigned>(grid)), dim3(kNormThreads), 0, st,
-                                 true, g, part + count);
-    if (e != cudaSuccess) return to_status(e);
-    count += static_cast<int>(grid);
+  int64_t chunks = fill_list(grads, nullptr, &at, &g, nullptr);
+  if (chunks == 0) return to_status(launch(grad_norm_none_kernel, dim3(1), dim3(1), 0, st, true, o));
+  o.total = static_cast<unsigned int>(list_grid(chunks));
+  if (at < grads->count) {
+    while (const int64_t more = fill_list(grads, nullptr, &at, &g, nullptr))
+      o.total += static_cast<unsigned int>(list_grid(more));
+    at = 0;
+    chunks = fill_list(grads, nullptr, &at, &g, nullptr);
   }
-  return to_status(launch(grad_norm_finish_kernel, dim3(1), dim3(kNormThreads), 0, st, true,
-                          static_cast<const double*>(part), count, max_norm, norm, coef));
+  while (true) {
+    const unsigned int grid = static_cast<unsigned int>(list_grid(chunks));
+    const cudaError_t e = launch(grad_norm_kernel, dim3(grid), dim3(kNormThreads), 0, st, true, g, o);
+    if (e != cudaSuccess) return to_status(e);
+    o.first += grid;
+    if (o.first == o.total) return QN_OK;
+    chunks = fill_list(grads, nullptr, &at, &g, nullptr);
+  }
 }
 
 qn_status qlora_grad_clip(const qn_tensor_list* grads, const qn_tensor_list* out, const float* coef,

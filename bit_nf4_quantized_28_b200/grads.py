@@ -55,9 +55,10 @@ def workspace_bytes(tensors):
 
 
 def make_workspace(tensors):
-    """Workspace of norm for a list of this length."""
+    """Workspace of norm for a list of this length; zeroed once (its first
+    256 bytes hold a counter, which every call leaves zero)."""
     tensors = _as_list(tensors)
-    return torch.empty(workspace_bytes(tensors), dtype=torch.uint8, device=tensors.device)
+    return torch.zeros(workspace_bytes(tensors), dtype=torch.uint8, device=tensors.device)
 
 
 def norm(tensors, max_norm=None, out=None, workspace=None):
@@ -75,7 +76,7 @@ def norm(tensors, max_norm=None, out=None, workspace=None):
     p = out.data_ptr()
     _run("qlora_grad_norm", dev, tensors.ref, 0.0 if max_norm is None else max_norm, p,
          None if max_norm is None else p + 4, ws.data_ptr(), ws.numel())
-    return out[0], None if max_norm is None else out[1]
+    return out.select(0, 0), None if max_norm is None else out.select(0, 1)
 
 
 def clip(tensors, coef, out=None):

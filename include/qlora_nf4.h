@@ -379,7 +379,9 @@ typedef struct {
  * gradient gives a non-finite norm; a NaN norm gives a NaN coef, an infinite
  * one 0.  norm, coef: fp32 in DEVICE memory (coef may be NULL; max_norm is
  * then ignored, else it is finite and >= 0).  An empty list has norm 0.
- * ws: at least qlora_grad_norm_workspace_bytes(count) bytes. */
+ * ws: at least qlora_grad_norm_workspace_bytes(count) bytes; its first
+ * 256 hold a counter: zero them once when the workspace is made; every call
+ * leaves them zero. */
 size_t qlora_grad_norm_workspace_bytes(int count);
 qn_status qlora_grad_norm(const qn_tensor_list* grads, float max_norm, float* norm, float* coef,
                           void* ws, size_t ws_bytes, qn_stream_t stream);

@@ -183,3 +183,13 @@ def test_refusals():
         grads.clip([t], c, out=[t, t])
     with pytest.raises(qn.QNError):
         grads.clip([t], c, out=[torch.ones(15, device="cuda")])
+
+
+def test_one_workspace_for_lists_of_any_length():
+    """A workspace made for the longest list serves the others too, in any
+    order: every call leaves its counter zero."""
+    short, long = _make([500, 70000], [F32, BF16], seed=9), _make([3000] * 1500, [F32] * 1500, seed=10)
+    ws = grads.make_workspace(long)
+    for ts in (short, long, short, [torch.empty(0, device="cuda")], long, long, short):
+        total, coef = grads.norm(ts, 0.3, workspace=ws)
+        _check(ts, 0.3, total, coef)
