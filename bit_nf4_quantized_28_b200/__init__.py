@@ -159,6 +159,14 @@ def _arg(t, what, dtype, shape, device=None):
                      f"{t.device}, strides {t.stride()}")
 
 
+def _out(t, what, dtype, shape, device):
+    """An output: the given tensor, checked, or a new one; and its address."""
+    if t is not None:
+        return t, _arg(t, what, dtype, shape, device)
+    t = torch.empty(shape, dtype=dtype, device=device)
+    return t, t.data_ptr()
+
+
 def _run(name, device, *args):
     """Calls `name` with the current stream of `device` (made current for the call)."""
     fn = getattr(lib(), name)

@@ -18,7 +18,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _arg, _run
+from . import _arg, _out, _run
 from . import merge as _merge
 
 BF16, F32, I8 = torch.bfloat16, torch.float32, torch.int8
@@ -38,11 +38,12 @@ def quantize(x, codes=None, scale=None):
     stands for x."""
     if x.dim() != 2:
         raise ValueError(f"x: [m, k] is needed, got {tuple(x.shape)}")
-    m, k = x.shape
-    codes = torch.empty(m, k, dtype=I8, device=x.device) if codes is None else codes
-    scale = torch.empty(m, dtype=F32, device=x.device) if scale is None else scale
-    _run("int8_quantize_rows", x.device, _arg(x, "x", BF16, x.shape), m, k, _arg(codes, "codes", I8, x.shape, x.device),
-         _arg(scale, "scale", F32, x.shape[:1], x.device))
+    m, k = shape = x.shape
+    dev = x.device
+    px = _arg(x, "x", BF16, shape)
+    codes, pc = _out(codes, "codes", I8, shape, dev)
+    scale, ps = _out(scale, "scale", F32, (m,), dev)
+    _run("int8_quantize_rows", dev, px, m, k, pc, ps)
     return codes, scale
 
 
@@ -63,10 +64,10 @@ def linear(codes, scale, w, y=None):
     """y = (codes w.codes^T) * scale * w.scale as bf16 [m, n_out]."""
     if codes.dim() != 2:
         raise ValueError(f"codes: [m, k] is needed, got {tuple(codes.shape)}")
-    m = codes.shape[0]
+    m, n, k = codes.shape[0], w.n_out, w.k_in
     dev = codes.device
-    y = torch.empty(m, w.n_out, dtype=BF16, device=dev) if y is None else y
-    _run("int8_linear_fwd", dev, _arg(codes, "codes", I8, (m, w.k_in)), _arg(scale, "scale", F32, (m,), dev), m,
-         _arg(w.codes, "w.codes", I8, (w.n_out, w.k_in), dev), _arg(w.scale, "w.scale", F32, (w.n_out,), dev),
-         w.n_out, w.k_in, _arg(y, "y", BF16, (m, w.n_out), dev))
+    pc, ps = _arg(codes, "codes", I8, (m, k)), _arg(scale, "scale", F32, (m,), dev)
+    pw, pws = _arg(w.codes, "w.codes", I8, (n, k), dev), _arg(w.scale, "w.scale", F32, (n,), dev)
+    y, py = _out(y, "y", BF16, (m, n), dev)
+    _run("int8_linear_fwd", dev, pc, ps, m, pw, pws, n, k, py)
     return y

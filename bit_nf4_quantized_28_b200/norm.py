@@ -11,7 +11,7 @@ current stream.  Formulas and rounding: include/qlora_nf4.h.
 
 import torch
 
-from . import _arg, _run, lib
+from . import _arg, _out, _run, lib
 
 BF16, F32 = torch.bfloat16, torch.float32
 
@@ -25,8 +25,7 @@ def _inputs(x, weight, residual, h):
     pw = _arg(weight, "weight", BF16, x.shape[1:], dev)
     if residual is None:
         return px, None, pw, x, None
-    h = torch.empty_like(x) if h is None else h
-    return px, pr, pw, h, _arg(h, "h", BF16, x.shape, dev)
+    return px, pr, pw, *_out(h, "h", BF16, x.shape, dev)
 
 
 def forward(x, weight, residual=None, eps=1e-5, y=None, h=None, rstd=None):
@@ -35,10 +34,10 @@ def forward(x, weight, residual=None, eps=1e-5, y=None, h=None, rstd=None):
     residual."""
     px, pr, pw, h, ph = _inputs(x, weight, residual, h)
     m, d = x.shape
-    y = torch.empty_like(x) if y is None else y
-    rstd = torch.empty(m, dtype=F32, device=x.device) if rstd is None else rstd
-    _run("rmsnorm_fwd", x.device, px, pr, pw, m, d, eps, ph, _arg(y, "y", BF16, x.shape, x.device),
-         _arg(rstd, "rstd", F32, x.shape[:1], x.device))
+    dev = x.device
+    y, py = _out(y, "y", BF16, x.shape, dev)
+    rstd, ps = _out(rstd, "rstd", F32, (m,), dev)
+    _run("rmsnorm_fwd", dev, px, pr, pw, m, d, eps, ph, py, ps)
     return y, h, rstd
 
 
@@ -47,10 +46,10 @@ def forward_int8(x, weight, residual=None, eps=1e-5, codes=None, scale=None, h=N
     scale per row; codes * scale stands for y."""
     px, pr, pw, h, ph = _inputs(x, weight, residual, h)
     m, d = x.shape
-    codes = torch.empty(m, d, dtype=torch.int8, device=x.device) if codes is None else codes
-    scale = torch.empty(m, dtype=F32, device=x.device) if scale is None else scale
-    _run("rmsnorm_fwd_int8", x.device, px, pr, pw, m, d, eps, ph, _arg(codes, "codes", torch.int8, x.shape, x.device),
-         _arg(scale, "scale", F32, x.shape[:1], x.device))
+    dev = x.device
+    codes, pc = _out(codes, "codes", torch.int8, x.shape, dev)
+    scale, ps = _out(scale, "scale", F32, (m,), dev)
+    _run("rmsnorm_fwd_int8", dev, px, pr, pw, m, d, eps, ph, pc, ps)
     return codes, scale, h
 
 
@@ -66,17 +65,19 @@ def backward(dy, h, weight, rstd, dh=None, need_dw=False, out=None, workspace=No
     if h.dim() != 2:
         raise ValueError(f"h: [m, d] is needed, got {tuple(h.shape)}")
     dev = h.device
-    m, d = h.shape
-    dx, dw = out if out is not None else (torch.empty_like(h), torch.empty(d, dtype=F32, device=dev) if need_dw else None)
+    m, d = shape = h.shape
+    dx, dw = out if out is not None else (None, None)
+    need_dw = dw is not None if out is not None else need_dw
+    args = (_arg(dy, "dy", BF16, shape, dev), _arg(h, "h", BF16, shape), _arg(weight, "weight", BF16, (d,), dev),
+            _arg(rstd, "rstd", F32, (m,), dev), _arg(dh, "dh", BF16, shape, dev))
+    dx, px = _out(dx, "dx", BF16, shape, dev)
+    dw, pw = _out(dw, "dw", F32, (d,), dev) if need_dw else (None, None)
     nbytes = 0
-    if dw is not None:
+    if need_dw:
         nbytes = backward_workspace_bytes(m, d) if workspace is None else workspace.numel()
         if workspace is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         elif workspace.dtype is not torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace: a contiguous uint8 tensor on {dev} is needed")
-    _run("rmsnorm_bwd", dev, _arg(dy, "dy", BF16, h.shape, dev), _arg(h, "h", BF16, h.shape),
-         _arg(weight, "weight", BF16, h.shape[1:], dev), _arg(rstd, "rstd", F32, h.shape[:1], dev),
-         _arg(dh, "dh", BF16, h.shape, dev), m, d, _arg(dx, "dx", BF16, h.shape, dev),
-         _arg(dw, "dw", F32, h.shape[1:], dev), None if dw is None else workspace.data_ptr(), nbytes)
+    _run("rmsnorm_bwd", dev, *args, m, d, px, pw, workspace.data_ptr() if need_dw else None, nbytes)
     return dx, dw

@@ -13,6 +13,13 @@ Cases (seeded synthetic inputs, the shapes the benchmark times):
   dequantize NF4 -> bf16 W_hat of a 4096 x 4096 weight
   merge      LoRA merge W_hat + (alpha / r) B A, 4096 x 4096, rank 16, alpha 16
   adamw8     8-bit AdamW step over a 7B model's adapters (rank 16, all linears: 39,976,960 values)
+  grad_norm  global norm of the same adapters' gradients, 448 tensors
+  norm_int8  RMS norm with residual and 8-bit output, 8192 x 4096
+  norm_bwd   backward of the norm with dw, 8192 x 4096
+  rows_int8  rows to 8 bits, 8192 x 4096
+  int8_t1    8-bit linear, 1 token, W 11008 x 4096
+  int8_t100  8-bit linear, 100 tokens, W 4096 x 4096
+  int8_gemm  8-bit linear, 2048 tokens, W 11008 x 4096
 
 Each launch is a plain library call (no CUDA graph), so a profiler sees the
 kernels one by one; the process synchronizes once at the end.
@@ -24,10 +31,11 @@ import sys
 import torch
 
 import bit_nf4_quantized_28_b200 as qn
+from bit_nf4_quantized_28_b200 import grads, int8, norm
 from bit_nf4_quantized_28_b200 import workloads as wl
 
 CASES = ("gemm_fwd", "gemm_dx", "train", "train_dropout", "gemv_t1", "gemv_t16", "quantize", "dequantize",
-         "merge", "adamw8")
+         "merge", "adamw8", "grad_norm", "norm_int8", "norm_bwd", "rows_int8", "int8_t1", "int8_t100", "int8_gemm")
 
 
 def main(argv=None):
@@ -76,6 +84,32 @@ def main(argv=None):
         pb = torch.empty(n, dtype=torch.bfloat16, device=dev)
         for t in range(1, args.launches + 1):
             qn.adamw8_step(p, grad, st, t, lr=2e-4, weight_decay=0.01, param_bf16=pb)
+    elif args.case == "grad_norm":
+        sizes = [v for _ in range(32) for _, n, k in wl.BLOCK7B for v in (16 * k, n * 16)]
+        gen = torch.Generator(device=dev).manual_seed(5)
+        tensors = grads.TensorList(torch.split(torch.randn(sum(sizes), generator=gen, device=dev), sizes))
+        ws = grads.make_workspace(tensors)
+        for _ in range(args.launches):
+            grads.norm(tensors, 0.3, workspace=ws)
+    elif args.case in ("norm_int8", "norm_bwd", "rows_int8"):
+        gen = torch.Generator(device=dev).manual_seed(7)
+        x, res, dy = (torch.randn(8192, 4096, generator=gen, device=dev).to(torch.bfloat16) for _ in range(3))
+        weight = torch.ones(4096, dtype=torch.bfloat16, device=dev)
+        rstd = torch.ones(8192, device=dev)
+        for _ in range(args.launches):
+            if args.case == "norm_int8":
+                norm.forward_int8(x, weight, res)
+            elif args.case == "norm_bwd":
+                norm.backward(dy, x, weight, rstd, dh=res, need_dw=True)
+            else:
+                int8.quantize(x)
+    elif args.case in ("int8_t1", "int8_t100", "int8_gemm"):
+        m, n, k = {"int8_t1": (1, 11008, 4096), "int8_t100": (100, 4096, 4096), "int8_gemm": (2048, 11008, 4096)}[args.case]
+        gen = torch.Generator(device=dev).manual_seed(8)
+        codes, scale = int8.quantize(torch.randn(m, k, generator=gen, device=dev).to(torch.bfloat16))
+        w = int8.quantize_weight((0.02 * torch.randn(n, k, generator=gen, device=dev)).to(torch.bfloat16))
+        for _ in range(args.launches):
+            int8.linear(codes, scale, w)
     elif args.case in ("dequantize", "merge"):
         W = wl.quant_weight().to(dev)
         w = qn.quantize(W)
