@@ -1652,10 +1652,40 @@ cudaError_t run_int8_vec(const Int8Params& p, cudaStream_t st) {
                 dim3(wide ? 256 : 128), 0, st, true, p);
 }
 
+// Clusters of `c` CTAs of the few-token kernel (one per SM) that fit the
+// current device at once.
+constexpr int kFewMaxSplits = 8;
+constexpr size_t kFewSmem = 232448 - 1024;     // (1 KB for the static part)
+
+int few_clusters(int c) {
+  static std::atomic<int> cached[64][kFewMaxSplits + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = cached[dev][c].load();
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = kFewSmem;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = c;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, int8_few_kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    cached[dev][c].store(n);
+  }
+  return n;
+}
+
 // Few tokens: 128-channel tiles, k split over a cluster.
 cudaError_t run_int8_few(const Int8Params& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  constexpr size_t kFewSmem = 232448 - 1024;     // (1 KB for the static part)
   if (!set_smem_here(int8_few_kernel, kFewSmem, &done)) return cudaErrorInvalidValue;
   Int8FewParams f = {};
   f.xs = p.xs;
@@ -1671,7 +1701,14 @@ cudaError_t run_int8_few(const Int8Params& p, cudaStream_t st) {
   f.tmem_cols = 32;
   while (f.tmem_cols < static_cast<uint32_t>(f.nt)) f.tmem_cols *= 2;
   const int64_t tiles = t_tiles * f.n_tiles;
-  f.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sm_count() / tiles, 8, f.ksteps})));
+  // As many splits as keep every cluster resident at once, with at least four
+  // k-blocks each.  (Clusters of 7 and 8 leave many SMs of a group unused: 15
+  // fit, so that 21 tiles of 7 splits took two rounds, 18.8 us for 815 x 320
+  // x 8048, where 6 splits take 10.4.  182 x 904 x 8624: 24.7 us unsplit, 9.0
+  // with 6.  157 x 4120 x 928, 8 k-blocks: 5.0 unsplit, 5.7 with 2.)
+  f.splits = 1;
+  for (int c = 2; c <= kFewMaxSplits && 4 * c <= f.ksteps; ++c)
+    if (tiles <= few_clusters(c)) f.splits = c;
   // Shared memory: the ring (later the sums of this CTA) and what the
   // partners send.  One CTA per SM, or two where there are more CTAs than SMs.
   const size_t stage = 16384 + static_cast<size_t>(f.nt) * 128;
