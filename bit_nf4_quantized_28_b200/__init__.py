@@ -412,10 +412,9 @@ def adamw8_step(param, grad, state, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, 
     if grad_scale is not None and (grad_scale.dtype is not torch.float32 or grad_scale.numel() != 1
                                    or grad_scale.device != param.device):
         raise ValueError(f"grad_scale: one fp32 value on {param.device} is needed")
-    _check(lib().qlora_adamw8_step_scaled(_ptr(param), _ptr(grad), _ptr(grad_scale), n, _ptr(state.m_codes),
-                                          _ptr(state.m_scale), _ptr(state.v_codes), _ptr(state.v_scale),
-                                          _ptr(param_bf16), float(lr), float(beta1), float(beta2), float(eps),
-                                          float(weight_decay), int(step), _stream()), "qlora_adamw8_step")
+    _run("qlora_adamw8_step_scaled", param.device, _ptr(param), _ptr(grad), _ptr(grad_scale), n, _ptr(state.m_codes),
+         _ptr(state.m_scale), _ptr(state.v_codes), _ptr(state.v_scale), _ptr(param_bf16), float(lr), float(beta1),
+         float(beta2), float(eps), float(weight_decay), int(step))
 
 
 # ------------------------------------------------------------------ failure detection

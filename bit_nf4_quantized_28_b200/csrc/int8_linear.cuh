@@ -10,7 +10,7 @@
 
 namespace qn {
 
-constexpr int64_t kInt8MaxK = (int64_t{1} << 17) - 16;
+constexpr int64_t kInt8EndK = int64_t{1} << 17;      // k is below this
 
 struct Int8Params {
   const int8_t* x;       // [m, k]

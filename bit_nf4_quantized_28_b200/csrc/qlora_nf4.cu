@@ -218,6 +218,7 @@ bool tmap_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
 // ------------------------------------------------------------------ checks
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
@@ -1518,7 +1519,7 @@ qn_status rmsnorm_fwd(const void* x, const void* residual, const void* weight, i
   qn_status s = norm_checks(x, residual, weight, m, d, eps, h);
   if (s != QN_OK || m == 0) return s;
   if (!y) return QN_ERR_ARG;
-  if (!aligned16(y) || !aligned16(rstd)) return QN_ERR_ALIGN;
+  if (!aligned16(y) || !aligned4(rstd)) return QN_ERR_ALIGN;
   if (!device_is_sm100()) return QN_ERR_UNSUPPORTED;
   RowParams p = row_params(x, residual, weight, m, d, eps, h);
   p.y = static_cast<__nv_bfloat16*>(y);
@@ -1533,7 +1534,7 @@ qn_status rmsnorm_fwd_int8(const void* x, const void* residual, const void* weig
   qn_status s = norm_checks(x, residual, weight, m, d, eps, h);
   if (s != QN_OK || m == 0) return s;
   if (!codes || !scale) return QN_ERR_ARG;
-  if (!aligned16(codes) || !aligned16(scale)) return QN_ERR_ALIGN;
+  if (!aligned8(codes) || !aligned4(scale)) return QN_ERR_ALIGN;
   if (!device_is_sm100()) return QN_ERR_UNSUPPORTED;
   RowParams p = row_params(x, residual, weight, m, d, eps, h);
   p.q = codes;
@@ -1554,7 +1555,7 @@ qn_status rmsnorm_bwd(const void* dy, const void* h, const void* weight, const f
   if (s != QN_OK) return s;
   if (m == 0 && !dw) return QN_OK;
   if (m > 0 && (!dy || !h || !weight || !rstd || !dx)) return QN_ERR_ARG;
-  if (m > 0 && (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(rstd) || !aligned16(dh) ||
+  if (m > 0 && (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned4(rstd) || !aligned16(dh) ||
                 !aligned16(dx)))
     return QN_ERR_ALIGN;
   if (!aligned16(dw)) return QN_ERR_ALIGN;
@@ -1608,14 +1609,17 @@ qn_status rmsnorm_bwd(const void* dy, const void* h, const void* weight, const f
 
 qn_status int8_quantize_rows(const void* x, int64_t m, int64_t k, int8_t* codes, float* scale, qn_stream_t stream) {
   clear_detail();
-  qn_status s = check_rows(m, k);
-  if (s != QN_OK || m == 0) return s;
+  if (m < 0 || k <= 0 || k % 8 != 0 || k >= kInt8EndK) return QN_ERR_SHAPE;
+  if (m == 0) return QN_OK;
   if (!x || !codes || !scale) return QN_ERR_ARG;
-  if (!aligned16(x) || !aligned16(codes) || !aligned16(scale)) return QN_ERR_ALIGN;
+  if (!aligned16(x) || !aligned8(codes) || !aligned4(scale)) return QN_ERR_ALIGN;
   if (!device_is_sm100()) return QN_ERR_UNSUPPORTED;
   RowParams p = row_params(x, nullptr, nullptr, m, k, 0.f, nullptr);
   p.q = codes;
   p.scale = scale;
+  if (k > kRowMaxCols)
+    return to_status(launch(row_quant_long_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(m, int64_t{1} << 30))),
+                            dim3(1024), 0, reinterpret_cast<cudaStream_t>(stream), true, p));
   const int nv = row_nv(m, k, 128, 8);
   return to_status(launch_rows(nv == 1   ? row_quant_kernel<1>
                                : nv == 2 ? row_quant_kernel<2>
@@ -1763,12 +1767,12 @@ extern "C" qn_status int8_linear_fwd(const int8_t* x_codes, const float* x_scale
                                      const float* w_scale, int64_t n, int64_t k, void* y, qn_stream_t stream) {
   clear_detail();
   // (coordinates and tile counts stay below 2^31)
-  if (m < 0 || n <= 0 || n % 8 != 0 || n > (int64_t{1} << 30) || k <= 0 || k % 16 != 0 || k > kInt8MaxK ||
+  if (m < 0 || n <= 0 || n % 8 != 0 || n > (int64_t{1} << 30) || k <= 0 || k % 16 != 0 || k >= kInt8EndK ||
       m > (int64_t{1} << 30))
     return QN_ERR_SHAPE;
   if (m == 0) return QN_OK;
   if (!x_codes || !x_scale || !w_codes || !w_scale || !y) return QN_ERR_ARG;
-  if (!aligned16(x_codes) || !aligned16(x_scale) || !aligned16(w_codes) || !aligned16(w_scale) || !aligned16(y))
+  if (!aligned16(x_codes) || !aligned4(x_scale) || !aligned16(w_codes) || !aligned16(w_scale) || !aligned16(y))
     return QN_ERR_ALIGN;
   if (!device_is_sm100()) return QN_ERR_UNSUPPORTED;
   Int8Params p = {};

@@ -157,9 +157,25 @@ __device__ __forceinline__ void store_codes(int8_t* out, float (&t)[8], const Ro
 }
 
 __device__ __forceinline__ float row_scale_value(uint32_t amax_bits, float rstd) {
+  if (amax_bits == 0u) return 0.f;      // (rstd of a row of zeros is infinite when eps is 0)
   return amax_bits >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
                                   : __fdiv_rn(__uint_as_float(amax_bits) * rstd, 127.f);
 }
+
+// The larger of two pairs of bf16 magnitudes (sign bits off: they order as
+// unsigned 16-bit integers, NaN above infinity above the finite).
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t u) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(u & 0x7FFF7FFFu));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t max_vec(uint32_t a, const uint4& v) {
+  return max_pair(max_pair(max_pair(max_pair(a, v.x), v.y), v.z), v.w);
+}
+
+// The larger half as the bits of an fp32 value.
+__device__ __forceinline__ uint32_t pair_top(uint32_t a) { return max(a << 16, a & 0xFFFF0000u); }
 
 template <int NV, bool kRes, bool kInt8>
 __global__ void __launch_bounds__(row_max_threads(NV)) row_kernel(RowParams p) {
@@ -241,9 +257,8 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_kernel(RowParams p) {
 }
 
 // Rows to 8 bits without a norm.  The values stay packed (two to a register)
-// until they are quantized: bf16 magnitudes order as unsigned 16-bit integers,
-// so the row's largest is found two at a time, and few registers let more
-// rows share an SM.
+// until they are quantized, so that the row's largest is found two at a time
+// and few registers let more rows share an SM.
 template <int NV>
 __global__ void __launch_bounds__(row_max_threads(NV)) row_quant_kernel(RowParams p) {
   __shared__ float fbuf[2][32];
@@ -263,13 +278,8 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_quant_kernel(RowParam
     }
     uint32_t two = 0u;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const uint32_t u[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        asm("max.u16x2 %0, %1, %2;" : "=r"(two) : "r"(two), "r"(u[j] & 0x7FFF7FFFu));
-    }
-    uint32_t amax = max(two << 16, two & 0xFFFF0000u);
+    for (int i = 0; i < NV; ++i) two = max_vec(two, hv[i]);
+    uint32_t amax = pair_top(two);
     float none = 0.f;
     block_sum_max(none, amax, fbuf[par], ubuf[par], nw);
     const RowScale s = row_scale(amax);
@@ -281,6 +291,34 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_quant_kernel(RowParam
       float f[8];
       unpack8(hv[i], f);
       store_codes(p.q + base + 8 * v, f, s);
+    }
+  }
+}
+
+// The same for rows too long for a CTA's registers: read twice, the second
+// time from L2.
+__global__ void __launch_bounds__(1024) row_quant_long_kernel(RowParams p) {
+  __shared__ float fbuf[2][32];
+  __shared__ uint32_t ubuf[2][32];
+  const int nvec = p.d >> 3;
+  int par = 0;
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x, par ^= 1) {
+    const uint4* x = reinterpret_cast<const uint4*>(p.x + row * p.d);
+    uint32_t two = 0u;
+#pragma unroll 4
+    for (int v = threadIdx.x; v < nvec; v += blockDim.x) two = max_vec(two, x[v]);
+    uint32_t amax = pair_top(two);
+    float none = 0.f;
+    block_sum_max(none, amax, fbuf[par], ubuf[par], blockDim.x >> 5);
+    const RowScale s = row_scale(amax);
+    if (threadIdx.x == 0) p.scale[row] = row_scale_value(amax, 1.f);
+#pragma unroll 2
+    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+      float f[8];
+      unpack8(x[v], f);
+      store_codes(p.q + row * p.d + 8 * v, f, s);
     }
   }
 }

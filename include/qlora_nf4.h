@@ -106,7 +106,7 @@ void nf4_levels(float out[16]);
  * synchronizes the device first).  *flags_out (HOST) receives the OR of the
  * bits set since the last read; 0 means no bounded wait gave up.  Bits: 1 a
  * wait of the tensor-core GEMM, 2 of the decode GEMV, 4 of a rank-r kernel,
- * 32 of the 8-bit linear, QN_WAIT_SELFTEST of qn_selftest_bounded_wait. */
+ * 32 of the 8-bit linear, 64 of the norm's backward, QN_WAIT_SELFTEST of qn_selftest_bounded_wait. */
 qn_status qn_device_error(int* flags_out);
 
 /* Failure-detection self-test: enqueues one warp whose thread 0 waits on a
@@ -353,7 +353,8 @@ qn_status qlora_adamw8_step(float* param, const float* grad, int64_t n,
 /* qlora_adamw8_step with the gradient multiplied by *grad_scale (one fp32
  * value in DEVICE memory, 4-byte aligned; NULL: 1) as it is read: the
  * clipping coefficient of qlora_grad_norm, with no pass over the gradients
- * of its own.  The product is rounded to fp32 before the step. */
+ * of its own.  The product is rounded to fp32 before the step.  A NaN factor
+ * makes every parameter NaN. */
 qn_status qlora_adamw8_step_scaled(float* param, const float* grad, const float* grad_scale, int64_t n,
                                    uint8_t* m_codes, float* m_scale, uint8_t* v_codes, float* v_scale,
                                    void* param_bf16, float lr, float beta1, float beta2, float eps,
@@ -402,7 +403,10 @@ qn_status qlora_grad_clip(const qn_tensor_list* grads, const qn_tensor_list* out
  * bf16 [d]; d % 8 == 0, d <= 32768 (QN_ERR_SHAPE otherwise); eps >= 0.
  * residual NULL: h is not written (may be NULL).  h may be x or residual, y
  * may be x when h is another tensor or not written.
- * rstd: NULL, or fp32 [m] for the backward. */
+ * rstd: NULL, or fp32 [m] for the backward.
+ * (In this and the following calls, values that stand one per row need
+ * 4-byte and codes that are written 8-byte alignment only, so that rows of a
+ * larger batch can be passed.) */
 qn_status rmsnorm_fwd(const void* x, const void* residual, const void* weight, int64_t m, int64_t d, float eps,
                       void* h, void* y, float* rstd, qn_stream_t stream);
 
@@ -430,8 +434,8 @@ qn_status rmsnorm_bwd(const void* dy, const void* h, const void* weight, const f
 
 /* Rows to 8 bits with one scale each: amax = max |x| of the row,
  * codes = rint(127 x / amax) (rounded as in rmsnorm_fwd_int8), scale =
- * amax / 127.  x bf16 [m, k], codes int8 [m, k], scale fp32 [m]; k as d of
- * rmsnorm_fwd; zero and non-finite rows as in rmsnorm_fwd_int8.  Quantizes a
+ * amax / 127.  x bf16 [m, k], codes int8 [m, k], scale fp32 [m]; k % 8 == 0,
+ * k < 131072 (QN_ERR_SHAPE otherwise); zero and non-finite rows as in rmsnorm_fwd_int8.  Quantizes a
  * weight [n_out, k_in] (one scale per output channel), such as qlora_merge's,
  * and tokens that no norm precedes. */
 qn_status int8_quantize_rows(const void* x, int64_t m, int64_t k, int8_t* codes, float* scale, qn_stream_t stream);

@@ -10,7 +10,7 @@ import torch
 import bit_nf4_quantized_28_b200 as qn
 from bit_nf4_quantized_28_b200 import build, grads, int8, norm
 
-P, ODD = ctypes.c_void_p(4096), ctypes.c_void_p(4104)
+P, ODD, ODD4 = ctypes.c_void_p(4096), ctypes.c_void_p(4104), ctypes.c_void_p(4098)
 F = ctypes.c_float
 
 
@@ -32,8 +32,8 @@ def test_norm_refusals(L):
         assert f(x=None) == 1 and f(w=None) == 1
         assert f(r=P) == 1                                        # a residual needs h
         assert f(x=ODD) == 3 and f(w=ODD) == 3 and f(r=ODD, h=P) == 3 and f(r=P, h=ODD) == 3
-    assert fwd(y=None) == 1 and fwd(y=ODD) == 3 and fwd(rs=ODD) == 3
-    assert i8(q=None) == 1 and i8(s=None) == 1 and i8(q=ODD) == 3
+    assert fwd(y=None) == 1 and fwd(y=ODD) == 3 and fwd(rs=ODD4) == 3
+    assert i8(q=None) == 1 and i8(s=None) == 1 and i8(q=ODD4) == 3 and i8(s=ODD4) == 3
     assert L.rmsnorm_bwd_workspace_bytes(0, 64) == 0
     need = L.rmsnorm_bwd_workspace_bytes(1000, 64)
     assert need >= 64 * 4
@@ -42,21 +42,21 @@ def test_norm_refusals(L):
     assert bwd(m=0, dw=None) == 0
     assert bwd(m=-1) == 2 and bwd(d=20) == 2
     for k in ("dy", "h", "w", "rs", "dx"):
-        assert bwd(**{k: None}) == 1 and bwd(**{k: ODD}) == 3
+        assert bwd(**{k: None}) == 1 and bwd(**{k: ODD4 if k == "rs" else ODD}) == 3
     assert bwd(dh=ODD) == 3 and bwd(dw=ODD) == 3
     assert bwd(ws=None) == 4 and bwd(nb=need - 1) == 4 and bwd(ws=ODD) == 3
 
 
 def test_int8_refusals(L):
     q = lambda x=P, m=4, k=64, c=P, s=P: L.int8_quantize_rows(x, m, k, c, s, None)
-    assert q(m=0) == 0 and q(m=-1) == 2 and q(k=12) == 2 and q(k=32768 + 8) == 2
-    assert q(x=None) == 1 and q(c=None) == 1 and q(s=None) == 1 and q(x=ODD) == 3 and q(c=ODD) == 3
+    assert q(m=0) == 0 and q(m=-1) == 2 and q(k=12) == 2 and q(k=131072) == 2
+    assert q(x=None) == 1 and q(c=None) == 1 and q(s=None) == 1 and q(x=ODD) == 3 and q(c=ODD4) == 3
     lin = lambda x=P, xs=P, m=4, w=P, ws=P, n=64, k=64, y=P: L.int8_linear_fwd(x, xs, m, w, ws, n, k, y, None)
     assert lin(m=0) == 0 and lin(m=-1) == 2
     assert lin(n=0) == 2 and lin(n=12) == 2 and lin(k=24) == 2 and lin(k=0) == 2
     assert lin(k=131072) == 2                                     # sums could pass 2^31
     for a in ("x", "xs", "w", "ws", "y"):
-        assert lin(**{a: None}) == 1 and lin(**{a: ODD}) == 3
+        assert lin(**{a: None}) == 1 and lin(**{a: ODD4 if a == "xs" else ODD}) == 3
 
 
 def _list(data, n, dtype):

@@ -125,6 +125,16 @@ def test_streams_and_graph(m):
     assert qn.device_error() == 0
 
 
+@pytest.mark.parametrize("m", [3, 20, 300])
+def test_slices_of_a_batch(m):
+    """Tokens in the middle of a larger batch."""
+    x, xs, w, ws = _operands(m + 9, 264, 528, seed=6)
+    W = _weight(w, ws)
+    x, xs = x.cuda(), xs.cuda()
+    got = int8.linear(x[5:5 + m], xs[5:5 + m], W)
+    assert torch.equal(got, int8.linear(x, xs, W)[5:5 + m])
+
+
 def test_refusals():
     x, xs, w, ws = _operands(4, 16, 32)
     W = _weight(w, ws)

@@ -126,7 +126,7 @@ def test_backward(m, d, need_dw, with_dh):
     assert np.all(np.abs(_f64(dw) - rw) <= adds * U * mag + 1e-38)
 
 
-@pytest.mark.parametrize("m,k", [(1, 8), (3, 64), (5, 11008), (300, 4096), (4096, 264)])
+@pytest.mark.parametrize("m,k", [(1, 8), (3, 64), (5, 11008), (300, 4096), (4096, 264), (2, 32776), (3, 131064)])
 def test_quantize_rows(m, k):
     x, _, _ = _inputs(m, k, False, seed=20)
     codes, scale = int8.quantize(x.cuda())
@@ -192,6 +192,34 @@ def test_aliased_outputs_and_rows_behind_the_last():
     big[:m] = cr
     got, _ = norm.backward(dy, h0, cw, rstd0, dh=big[:m], out=(big[:m], None))
     assert torch.equal(got, want) and bool((big[m:] == 7).all())
+
+
+def test_zero_row_without_eps():
+    """eps = 0: a row of zeros still has scale 0 and codes 0."""
+    x, _, w = _inputs(4, 64, False, seed=60)
+    codes, scale, _ = norm.forward_int8(x.cuda(), w.cuda(), eps=0.0)
+    assert float(scale[1]) == 0 and not codes[1].any() and bool(torch.isfinite(scale).all())
+
+
+def test_slices_of_a_batch():
+    """Rows in the middle of larger buffers: codes and values stand on 16-byte
+    boundaries there, one-per-row values on 4-byte ones."""
+    x, res, w = _cuda(*_inputs(9, 72, True, seed=61))
+    y, h, rstd = norm.forward(x, w, res)
+    codes, scale, _ = norm.forward_int8(x, w, res)
+    q, s = int8.quantize(x)
+    dy = _bf16(62, 9, 72).cuda()
+    dx, _ = norm.backward(dy, h, w, rstd, dh=res)
+    big = [torch.zeros_like(t) for t in (y, h, rstd, codes, scale, q, s)]
+    a, b = 3, 8
+    cut = [t[a:b] for t in big]
+    norm.forward(x[a:b], w, res[a:b], y=cut[0], h=cut[1], rstd=cut[2])
+    norm.forward_int8(x[a:b], w, res[a:b], codes=cut[3], scale=cut[4], h=cut[1])
+    int8.quantize(x[a:b], codes=cut[5], scale=cut[6])
+    for t, want in zip(big, (y, h, rstd, codes, scale, q, s)):
+        assert torch.equal(t[a:b], want[a:b]) and not t[:a].any() and not t[b:].any()
+    got, _ = norm.backward(dy[a:b], h[a:b], w, rstd[a:b], dh=res[a:b])
+    assert torch.equal(got, dx[a:b])
 
 
 def test_no_rows():
