@@ -10,7 +10,10 @@
 // Squares and sums are fp64: they neither overflow (fp32 squares do beyond
 // 1.8e19) nor lose small gradients beside large ones.  The CTAs' sums are
 // added in a fixed order, so equal inputs give equal bits.  HBM-bound: each
-// gradient is read once.
+// gradient is read once.  Measured over the adapters of a 7B model (39,976,960
+// fp32 values): 27.1 us, 5.9 TB/s, whether in 448 tensors or in one; chunks of
+// 2048 or 8192 values measured the same.  Clipping them into other buffers:
+// 57.6 us, 5.6 TB/s.
 #pragma once
 
 #include "common.cuh"
@@ -61,8 +64,10 @@ __device__ __forceinline__ void each_value(int64_t lo, int64_t hi, F f) {
 
 // The CTA that is the last of the call's to leave its sum (a counter in the
 // workspace tells, and is back at zero after it) adds all of them in their
-// order and writes the norm and the coefficient: one launch per call, where a
-// second one for this cost 1.3 us on the device and 5 on the host.
+// order and writes the norm and the coefficient.  For the 14 gradients of one
+// layer (1.25 M values) a second launch for this took 4.4 us on the device
+// against 4.8 (the counter's round trip), but 3.4 us more on the host, which
+// is what bounds a call that small.
 struct NormOut {
   double* part;             // the call's sums, one per CTA
   unsigned int* counter;    // zero between calls
