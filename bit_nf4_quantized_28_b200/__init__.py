@@ -159,11 +159,12 @@ def _arg(t, what, dtype, shape, device=None):
                      f"{t.device}, strides {t.stride()}")
 
 
-def _out(t, what, dtype, shape, device):
-    """An output: the given tensor, checked, or a new one; and its address."""
+def _out(t, what, dtype, shape, device, like=None):
+    """An output: the given tensor, checked, or a new one (of the shape of
+    `like`, a checked tensor, where that is given: 1 us less); and its address."""
     if t is not None:
         return t, _arg(t, what, dtype, shape, device)
-    t = torch.empty(shape, dtype=dtype, device=device)
+    t = torch.empty(shape, dtype=dtype, device=device) if like is None else torch.empty_like(like, dtype=dtype)
     return t, t.data_ptr()
 
 

@@ -25,7 +25,7 @@
 // the rate of a plain copy), 8-bit output 37.4 us (6.3 TB/s; of 128-thread
 // CTAs with NV = 4: 42.9 with 256 threads and NV = 2), backward 39.9 us
 // (6.7 TB/s; NV = 2, where NV = 4 took 54.7 with half the threads), with dw
-// 48.8.  Rows to 8 bits 21.9 us (4.6 TB/s): its few bytes per value leave the
+// 46.5.  Rows to 8 bits 21.9 us (4.6 TB/s): its few bytes per value leave the
 // instructions visible (issue slots busy 71 %).  One row of 4096: 1.5 to 2 us.
 #pragma once
 
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_bwd_kernel(RowBwdPara
 // sums of its columns in registers, which leaves too few of them to hold the
 // next rows' loads.  So rows come through a ring in shared memory (bulk
 // copies of dy, h and dh, `stages` rows deep), and each is read there twice.
-// 8192 x 4096: 48.8 us, where loads to registers took 57.4; 2048 x 11008 38.3,
+// 8192 x 4096: 46.5 us, where loads to registers took 57.4; 2048 x 11008 38.4,
 // where they took 58.
 constexpr int kRowBwdMaxStages = 4;
 
@@ -448,6 +448,15 @@ __global__ void __launch_bounds__(1024) row_bwd_dw_kernel(RowBwdParams p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  // with one vector per thread its weights, and a row's dy and h between the
+  // two uses, fit the registers
+  constexpr bool kKeep = NV == 1;
+  uint4 wv = zero;
+  if (kKeep && threadIdx.x < nvec) wv = __ldg(reinterpret_cast<const uint4*>(p.w) + threadIdx.x);
+  auto weight = [&](int i) {
+    const int v = threadIdx.x + i * T;
+    return kKeep ? wv : (v < nvec ? __ldg(reinterpret_cast<const uint4*>(p.w) + v) : zero);
+  };
   int stage = 0, par = 0;
   uint32_t phase = 0;
   for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x, par ^= 1) {
@@ -457,14 +466,17 @@ __global__ void __launch_bounds__(1024) row_bwd_dw_kernel(RowBwdParams p) {
     const uint4* sdy = reinterpret_cast<const uint4*>(row_ring + stage * stage_bytes);
     const uint4* sh = sdy + nvec;
     const uint4* sdh = sh + nvec;
+    uint4 dyv[kKeep ? NV : 1], hv[kKeep ? NV : 1];
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = threadIdx.x + i * T;
+      const int v = threadIdx.x + i * T, r = kKeep ? i : 0;
+      dyv[r] = v < nvec ? sdy[v] : zero;
+      hv[r] = v < nvec ? sh[v] : zero;
       float a[8], b[8], c[8];
-      unpack8(v < nvec ? sdy[v] : zero, a);
-      unpack8(v < nvec ? sh[v] : zero, b);
-      unpack8(v < nvec ? __ldg(reinterpret_cast<const uint4*>(p.w) + v) : zero, c);
+      unpack8(dyv[r], a);
+      unpack8(hv[r], b);
+      unpack8(weight(i), c);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         dw[i][j] = fmaf(a[j], b[j] * rstd, dw[i][j]);
@@ -484,9 +496,9 @@ __global__ void __launch_bounds__(1024) row_bwd_dw_kernel(RowBwdParams p) {
       const int v = threadIdx.x + i * T;
       if (v >= nvec) continue;
       float a[8], b[8], c[8], e[8];
-      unpack8(sdy[v], a);
-      unpack8(sh[v], b);
-      unpack8(__ldg(reinterpret_cast<const uint4*>(p.w) + v), c);
+      unpack8(kKeep ? dyv[kKeep ? i : 0] : sdy[v], a);
+      unpack8(kKeep ? hv[kKeep ? i : 0] : sh[v], b);
+      unpack8(weight(i), c);
       unpack8(p.dh ? sdh[v] : zero, e);
 #pragma unroll
       for (int j = 0; j < 8; ++j) a[j] = fmaf(rstd, fmaf(-b[j], c1, a[j] * c[j]), e[j]);

@@ -68,7 +68,7 @@ def norm(tensors, max_norm=None, out=None, workspace=None):
     tensors = _as_list(tensors)
     dev = tensors.device
     out = torch.empty(2, dtype=torch.float32, device=dev) if out is None else out
-    if out.dtype is not torch.float32 or out.numel() != 2 or out.device != dev or not out.is_contiguous():
+    if out.dtype is not torch.float32 or out.shape != (2,) or out.device != dev or not out.is_contiguous():
         raise ValueError(f"out: two fp32 values on {dev} are needed")
     ws = make_workspace(tensors) if workspace is None else workspace
     if ws.device != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
@@ -76,7 +76,8 @@ def norm(tensors, max_norm=None, out=None, workspace=None):
     p = out.data_ptr()
     _run("qlora_grad_norm", dev, tensors.ref, 0.0 if max_norm is None else max_norm, p,
          None if max_norm is None else p + 4, ws.data_ptr(), ws.numel())
-    return out.select(0, 0), None if max_norm is None else out.select(0, 1)
+    total, coef = out.unbind(0)
+    return total, None if max_norm is None else coef
 
 
 def clip(tensors, coef, out=None):

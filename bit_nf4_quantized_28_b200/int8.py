@@ -41,7 +41,7 @@ def quantize(x, codes=None, scale=None):
     m, k = shape = x.shape
     dev = x.device
     px = _arg(x, "x", BF16, shape)
-    codes, pc = _out(codes, "codes", I8, shape, dev)
+    codes, pc = _out(codes, "codes", I8, shape, dev, x)
     scale, ps = _out(scale, "scale", F32, (m,), dev)
     _run("int8_quantize_rows", dev, px, m, k, pc, ps)
     return codes, scale

@@ -25,7 +25,7 @@ def _inputs(x, weight, residual, h):
     pw = _arg(weight, "weight", BF16, x.shape[1:], dev)
     if residual is None:
         return px, None, pw, x, None
-    return px, pr, pw, *_out(h, "h", BF16, x.shape, dev)
+    return px, pr, pw, *_out(h, "h", BF16, x.shape, dev, x)
 
 
 def forward(x, weight, residual=None, eps=1e-5, y=None, h=None, rstd=None):
@@ -35,7 +35,7 @@ def forward(x, weight, residual=None, eps=1e-5, y=None, h=None, rstd=None):
     px, pr, pw, h, ph = _inputs(x, weight, residual, h)
     m, d = x.shape
     dev = x.device
-    y, py = _out(y, "y", BF16, x.shape, dev)
+    y, py = _out(y, "y", BF16, x.shape, dev, x)
     rstd, ps = _out(rstd, "rstd", F32, (m,), dev)
     _run("rmsnorm_fwd", dev, px, pr, pw, m, d, eps, ph, py, ps)
     return y, h, rstd
@@ -47,7 +47,7 @@ def forward_int8(x, weight, residual=None, eps=1e-5, codes=None, scale=None, h=N
     px, pr, pw, h, ph = _inputs(x, weight, residual, h)
     m, d = x.shape
     dev = x.device
-    codes, pc = _out(codes, "codes", torch.int8, x.shape, dev)
+    codes, pc = _out(codes, "codes", torch.int8, x.shape, dev, x)
     scale, ps = _out(scale, "scale", F32, (m,), dev)
     _run("rmsnorm_fwd_int8", dev, px, pr, pw, m, d, eps, ph, pc, ps)
     return codes, scale, h
@@ -70,7 +70,7 @@ def backward(dy, h, weight, rstd, dh=None, need_dw=False, out=None, workspace=No
     need_dw = dw is not None if out is not None else need_dw
     args = (_arg(dy, "dy", BF16, shape, dev), _arg(h, "h", BF16, shape), _arg(weight, "weight", BF16, (d,), dev),
             _arg(rstd, "rstd", F32, (m,), dev), _arg(dh, "dh", BF16, shape, dev))
-    dx, px = _out(dx, "dx", BF16, shape, dev)
+    dx, px = _out(dx, "dx", BF16, shape, dev, h)
     dw, pw = _out(dw, "dw", F32, (d,), dev) if need_dw else (None, None)
     nbytes = 0
     if need_dw:
