@@ -393,6 +393,9 @@ __device__ __forceinline__ void umma_s8(uint32_t d_tmem, uint64_t a_desc, uint64
       : "memory");
 }
 
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
@@ -533,7 +536,7 @@ __global__ void __launch_bounds__(kFewThreads)
     }
     __syncwarp();
     have = __all_sync(0xFFFFFFFFu, bounded_wait<true>(&rx, 0, abort_flag, ERR_INT8_WAIT)) && have;
-    cluster_arrive();                              // what the partners sent here has been read
+    cluster_arrive_relaxed();                      // what the partners sent has arrived here
   }
   const int* const got = reinterpret_cast<const int*>(ring + p.recv);
   if (!have) abort_grace();
