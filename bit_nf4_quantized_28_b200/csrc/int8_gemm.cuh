@@ -356,12 +356,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 // by bulk copies between the CTAs' shared memories, each CTA finishing its
 // share of the tokens.
 //
-// Measured: 100 tokens x 4096 x 4096 9.0 us (18 MB: 2.7 at HBM's rate; 1.5 of
-// launch and first copy, 2 of the exchange and the output remain), 32 x 11008
-// x 4096 11.1 us, 16 x 4096 x 11008 11.3, 512 x 4096 x 4096 12.2.  Steps on
-// the way for the 100 tokens: 21.2 us in one 256 x 256 tile row of the kernel
-// above; 11.9 with k split and the sums written word by word to the partners;
-// 9.3 with bulk copies; 9.0 with the scales ahead.
+// Measured: 100 tokens x 4096 x 4096 8.6 us (18 MB: 2.7 at HBM's rate), 17
+// tokens 6.3, 32 x 11008 x 4096 11.2, 16 x 4096 x 11008 10.9 (45 MB: 6.9 at
+// HBM's rate), 512 x 4096 x 4096 12.4.  In cycles of the 100 tokens' CTA: the
+// first copy lands at 2,600, the last product ends at 6,900, its sums are in
+// shared memory at 8,100, the partners' at 10,500, the output leaves by
+// 12,100.  Steps on the way for the 100 tokens: 21.2 us in one row of 256 x
+// 256 tiles of the kernel above; 11.9 with k split and the sums written word
+// by word to the partners; 9.3 with bulk copies; 9.0 with the token scales
+// ahead; 8.6 with a last cluster barrier that releases nothing.
 //   warp 0      TMA producer (one lane)
 //   warp 1      MMA issuer (cta_group::1), owner of TMEM
 //   all warps   TMEM -> shared memory -> partners -> sum -> scales -> bf16
@@ -407,6 +410,7 @@ __global__ void __launch_bounds__(kFewThreads)
                     Int8FewParams p) {
   extern __shared__ uint8_t few_smem_raw[];
   __shared__ __align__(8) uint64_t full[kFewMaxStages], empty[kFewMaxStages], done, rx;
+  __shared__ __align__(16) float ws_s[128];
   __shared__ float xs_s[kFewTokens];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
@@ -494,16 +498,13 @@ __global__ void __launch_bounds__(kFewThreads)
     if (ok && elect_one()) umma_commit(&done);
     __syncwarp();
   }
-  // this thread's 8 channels of the final sums
-  const int g8 = (threadIdx.x & 15) * 8;
-  const bool ch_ok = ch0 + g8 < p.n;               // n is a multiple of 8
-  float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
-  if (ch_ok) {
-    s0 = __ldg(reinterpret_cast<const float4*>(p.ws + ch0 + g8));
-    s1 = __ldg(reinterpret_cast<const float4*>(p.ws + ch0 + g8) + 1);
+  // The scales go to shared memory while the products run.  (Loads into
+  // registers here were moved down to their use behind the exchange.)
+  if (threadIdx.x >= 128) {
+    const int i = static_cast<int>(threadIdx.x) - 128;
+    xs_s[i] = i < toks ? __ldg(p.xs + t0 + i) : 0.f;
+    ws_s[i] = ch0 + i < p.n ? __ldg(p.ws + ch0 + i) : 0.f;
   }
-  if (threadIdx.x >= 128 && static_cast<int>(threadIdx.x) - 128 < toks)
-    xs_s[threadIdx.x - 128] = __ldg(p.xs + t0 + threadIdx.x - 128);
   bool have = __all_sync(0xFFFFFFFFu, bounded_wait<false>(&done, 0, abort_flag, ERR_INT8_WAIT));
   tc_fence_after();
   // every product of this CTA is done and the ring is free: the sums go there, [token][channel]
@@ -539,25 +540,30 @@ __global__ void __launch_bounds__(kFewThreads)
     cluster_arrive_relaxed();                      // what the partners sent has arrived here
   }
   const int* const got = reinterpret_cast<const int*>(ring + p.recv);
+  // 16 threads per token, 4 channels of each half of the tile each: 16-byte
+  // reads of consecutive threads stand side by side (no bank conflicts)
+  const int c4 = (threadIdx.x & 15) * 4;
+  const bool in0 = ch0 + c4 < p.n, in1 = ch0 + 64 + c4 < p.n;      // n is a multiple of 8
+  const float4 s0 = *reinterpret_cast<const float4*>(ws_s + c4), s1 = *reinterpret_cast<const float4*>(ws_s + 64 + c4);
   if (!have) abort_grace();
-#pragma unroll 4
+#pragma unroll 2
   for (int i = threadIdx.x >> 4; i < (have ? mine : 0); i += kFewThreads / 16) {
-    const int4* src = reinterpret_cast<const int4*>(stage + (first + i) * 128 + g8);
-    int4 a = src[0], b = src[1];
+    const int* src = stage + (first + i) * 128 + c4;
+    int4 a = *reinterpret_cast<const int4*>(src), b = *reinterpret_cast<const int4*>(src + 64);
     for (int s = 0; s < splits - 1; ++s) {
-      src = reinterpret_cast<const int4*>(got + (s * mine + i) * 128 + g8);
-      const int4 u = src[0], w = src[1];
+      src = got + (s * mine + i) * 128 + c4;
+      const int4 u = *reinterpret_cast<const int4*>(src), w = *reinterpret_cast<const int4*>(src + 64);
       a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
       b.x += w.x; b.y += w.y; b.z += w.z; b.w += w.w;
     }
-    const int64_t row = t0 + first + i;
     const float x = xs_s[first + i];
-    uint4 o;
-    o.x = pack_bf16x2(__int2float_rn(a.x) * (x * s0.x), __int2float_rn(a.y) * (x * s0.y));
-    o.y = pack_bf16x2(__int2float_rn(a.z) * (x * s0.z), __int2float_rn(a.w) * (x * s0.w));
-    o.z = pack_bf16x2(__int2float_rn(b.x) * (x * s1.x), __int2float_rn(b.y) * (x * s1.y));
-    o.w = pack_bf16x2(__int2float_rn(b.z) * (x * s1.z), __int2float_rn(b.w) * (x * s1.w));
-    if (ch_ok) *reinterpret_cast<uint4*>(p.y + row * p.n + ch0 + g8) = o;
+    __nv_bfloat16* const y = p.y + (t0 + first + i) * p.n + ch0 + c4;
+    if (in0)
+      *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(__int2float_rn(a.x) * (x * s0.x), __int2float_rn(a.y) * (x * s0.y)),
+                                                pack_bf16x2(__int2float_rn(a.z) * (x * s0.z), __int2float_rn(a.w) * (x * s0.w)));
+    if (in1)
+      *reinterpret_cast<uint2*>(y + 64) = make_uint2(pack_bf16x2(__int2float_rn(b.x) * (x * s1.x), __int2float_rn(b.y) * (x * s1.y)),
+                                                     pack_bf16x2(__int2float_rn(b.z) * (x * s1.z), __int2float_rn(b.w) * (x * s1.w)));
   }
   __syncwarp();
   if (splits > 1) cluster_wait();                  // no CTA leaves before its copies have been read

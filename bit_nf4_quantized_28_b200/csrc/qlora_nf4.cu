@@ -1659,7 +1659,9 @@ cudaError_t run_int8_vec(const Int8Params& p, cudaStream_t st) {
 // Clusters of `c` CTAs of the few-token kernel (one per SM) that fit the
 // current device at once.
 constexpr int kFewMaxSplits = 8;
-constexpr size_t kFewSmem = 232448 - 1024;     // (1 KB for the static part)
+constexpr size_t kFewSmem = 232448 - 2048;     // dynamic (2 KB for the static part)
+
+constexpr size_t kFewSmemHalf = 110 * 1024;    // with two CTAs per SM (228 KB, 1 KB of it reserved per CTA)
 
 int few_clusters(int c) {
   static std::atomic<int> cached[64][kFewMaxSplits + 1];
@@ -1718,7 +1720,7 @@ cudaError_t run_int8_few(const Int8Params& p, cudaStream_t st) {
   const size_t stage = 16384 + static_cast<size_t>(f.nt) * 128;
   const size_t sums = static_cast<size_t>(round_up(f.tok, 32)) * 512;
   const size_t recv = static_cast<size_t>(f.splits - 1) * ceil_div(f.tok, f.splits) * 512;
-  const size_t room = (tiles * f.splits > sm_count() ? 113 * 1024 : kFewSmem) - 1024 - recv;
+  const size_t room = (tiles * f.splits > sm_count() ? kFewSmemHalf : kFewSmem) - 1024 - recv;
   f.stages = static_cast<int>(std::min<size_t>({room / stage, static_cast<size_t>(kFewMaxStages),
                                                 static_cast<size_t>(ceil_div(f.ksteps, f.splits))}));
   f.stages = std::max(1, f.stages);
