@@ -1,4 +1,10 @@
 // bounded_wait.cuh -- the barrier wait of the kernels beside the NF4 linear.
+//
+// A note that holds for all of those kernels: they may start before the kernel
+// ahead of them has ended, and read its results after griddepcontrol.wait with
+// plain loads.  Loads through the read-only path (__ldg) promise the compiler
+// data that never changes while the kernel runs, which would let it move them
+// ahead of that wait.
 #pragma once
 
 #include "common.cuh"

@@ -290,9 +290,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       int mt, nt;
       i8_tile(p, t, mt, nt);
       const int row0 = mt * kI8BM + static_cast<int>(rank) * 128 + wq * 32;
-      const float xs = row0 + lane < p.m ? __ldg(p.xs + row0 + lane) : 0.f;
+      const float xs = row0 + lane < p.m ? p.xs[row0 + lane] : 0.f;
       float ws = 0.f;
-      if (et < BN && static_cast<int64_t>(nt) * BN + et < p.n) ws = __ldg(p.ws + static_cast<int64_t>(nt) * BN + et);
+      if (et < BN && static_cast<int64_t>(nt) * BN + et < p.n) ws = p.ws[static_cast<int64_t>(nt) * BN + et];
       named_bar_sync(1, kI8EpiWarps * 32);      // the previous tile's scales have been used
       if (et < BN) scales[et] = ws;
       named_bar_sync(1, kI8EpiWarps * 32);
@@ -506,8 +506,8 @@ __global__ void __launch_bounds__(kFewThreads)
   // registers here were moved down to their use behind the exchange.)
   if (threadIdx.x >= 128) {
     const int i = static_cast<int>(threadIdx.x) - 128;
-    xs_s[i] = i < toks ? __ldg(p.xs + t0 + i) : 0.f;
-    ws_s[i] = ch0 + i < p.n ? __ldg(p.ws + ch0 + i) : 0.f;
+    xs_s[i] = i < toks ? p.xs[t0 + i] : 0.f;
+    ws_s[i] = ch0 + i < p.n ? p.ws[ch0 + i] : 0.f;
   }
   bool have = __all_sync(0xFFFFFFFFu, bounded_wait<false>(&done, 0, abort_flag, ERR_INT8_WAIT));
   tc_fence_after();

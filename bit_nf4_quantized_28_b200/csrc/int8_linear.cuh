@@ -80,18 +80,18 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 5) int8_vec_kernel(Int8Pa
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int ku = k + 64 * W * u + q * 16;
-        f.a[u] = __ldg(reinterpret_cast<const uint4*>(w0 + ku));
-        f.b[u] = __ldg(reinterpret_cast<const uint4*>(w1 + ku));
-        f.x[u] = tok ? __ldg(reinterpret_cast<const uint4*>(xr + ku)) : zero;
+        f.a[u] = *reinterpret_cast<const uint4*>(w0 + ku);
+        f.b[u] = *reinterpret_cast<const uint4*>(w1 + ku);
+        f.x[u] = tok ? *reinterpret_cast<const uint4*>(xr + ku) : zero;
       }
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int ku = k + 64 * W * u + q * 16;
         const bool in = ku < kend;
-        f.a[u] = in ? __ldg(reinterpret_cast<const uint4*>(w0 + ku)) : zero;
-        f.b[u] = in ? __ldg(reinterpret_cast<const uint4*>(w1 + ku)) : zero;
-        f.x[u] = in && tok ? __ldg(reinterpret_cast<const uint4*>(xr + ku)) : zero;
+        f.a[u] = in ? *reinterpret_cast<const uint4*>(w0 + ku) : zero;
+        f.b[u] = in ? *reinterpret_cast<const uint4*>(w1 + ku) : zero;
+        f.x[u] = in && tok ? *reinterpret_cast<const uint4*>(xr + ku) : zero;
       }
     }
   };

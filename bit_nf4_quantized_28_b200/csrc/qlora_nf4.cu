@@ -4,7 +4,10 @@
 // and kernel launches.  Every launch after the first of a call uses
 // programmatic stream serialization, so a kernel's prologue overlaps the
 // tail of its predecessor; each kernel waits for its predecessor
-// (griddepcontrol.wait) before touching global memory.
+// (griddepcontrol.wait) before touching global memory.  The optimizer step
+// and the operators beside the linear (norm, 8-bit rows and linear, gradient
+// norm and clipping) launch that way from the first, behind whatever kernel
+// precedes them in the stream: all their threads wait before any access.
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -130,7 +133,7 @@ bool device_is_sm100() {
 // ------------------------------------------------------------------ launches
 
 // Launches `kernel`; `pdl` lets it start while its predecessor in the stream
-// (always a kernel of this library within the same call) finishes, and
+// finishes (it must then wait for it before touching global memory), and
 // `cluster` > 1 groups consecutive CTAs into thread-block clusters.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_ex(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,

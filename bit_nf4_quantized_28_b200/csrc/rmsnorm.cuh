@@ -19,10 +19,10 @@
 // vectors of 8 values (16-byte accesses), thread tid the vectors tid + i T.
 // One row per CTA and many CTAs per SM, which cover one another's reductions:
 // persistent CTAs that load the next row ahead measured slower (8192 x 4096,
-// 8-bit output: 43.7 to 49.8 us against 37.4), for the registers they take.
+// 8-bit output: 43.7 to 49.8 us against 36.6), for the registers they take.
 //
 // Measured at 8192 x 4096 with the residual: bf16 output 41.1 us (6.5 TB/s,
-// the rate of a plain copy), 8-bit output 37.4 us (6.3 TB/s; of 128-thread
+// the rate of a plain copy), 8-bit output 36.6 us (6.4 TB/s; of 128-thread
 // CTAs with NV = 4: 42.9 with 256 threads and NV = 2), backward 39.9 us
 // (6.7 TB/s; NV = 2, where NV = 4 took 54.7 with half the threads), with dw
 // 46.5.  Rows to 8 bits 21.9 us (4.6 TB/s): its few bytes per value leave the
@@ -205,6 +205,14 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_kernel(RowParams p) {
       const int v = threadIdx.x + i * T;
       hv[i] = v < nvec ? *reinterpret_cast<const uint4*>(p.x + base + 8 * v) : make_uint4(0u, 0u, 0u, 0u);
     }
+    auto weight = [&](int v) {
+      return v < nvec ? reinterpret_cast<const uint4*>(p.w)[v] : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 wv[kInt8 ? NV : 1];                 // (loaded ahead of h's stores, which they could not pass)
+    if constexpr (kInt8) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) wv[i] = weight(threadIdx.x + i * T);
+    }
     if constexpr (kRes) {
       uint4 rv[NV];
 #pragma unroll
@@ -219,16 +227,13 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_kernel(RowParams p) {
         if (v < nvec) *reinterpret_cast<uint4*>(p.h + base + 8 * v) = hv[i];
       }
     }
-    auto weight = [&](int v) {
-      return v < nvec ? __ldg(reinterpret_cast<const uint4*>(p.w) + v) : make_uint4(0u, 0u, 0u, 0u);
-    };
     float t[kInt8 ? NV : 1][8];
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float f[8], wf[8];
       unpack8(hv[i], f);
-      if constexpr (kInt8) unpack8(weight(threadIdx.x + i * T), wf);
+      if constexpr (kInt8) unpack8(wv[i], wf);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         ssq = fmaf(f[j], f[j], ssq);
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_bwd_kernel(RowBwdPara
       float a[8], b[8], c[8];
       unpack8(dyv[i], a);
       unpack8(hv[i], b);
-      unpack8(v < nvec ? __ldg(reinterpret_cast<const uint4*>(p.w) + v) : zero, c);
+      unpack8(v < nvec ? reinterpret_cast<const uint4*>(p.w)[v] : zero, c);
 #pragma unroll
       for (int j = 0; j < 8; ++j) dot = fmaf(a[j] * c[j], b[j], dot);
     }
@@ -391,7 +396,7 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_bwd_kernel(RowBwdPara
       float a[8], b[8], c[8], e[8];
       unpack8(dyv[i], a);
       unpack8(hv[i], b);
-      unpack8(__ldg(reinterpret_cast<const uint4*>(p.w) + v), c);
+      unpack8(reinterpret_cast<const uint4*>(p.w)[v], c);
       unpack8(av[i], e);
 #pragma unroll
       for (int j = 0; j < 8; ++j) a[j] = fmaf(rstd, fmaf(-b[j], c1, a[j] * c[j]), e[j]);
@@ -452,15 +457,15 @@ __global__ void __launch_bounds__(1024) row_bwd_dw_kernel(RowBwdParams p) {
   // two uses, fit the registers
   constexpr bool kKeep = NV == 1;
   uint4 wv = zero;
-  if (kKeep && threadIdx.x < nvec) wv = __ldg(reinterpret_cast<const uint4*>(p.w) + threadIdx.x);
+  if (kKeep && threadIdx.x < nvec) wv = reinterpret_cast<const uint4*>(p.w)[threadIdx.x];
   auto weight = [&](int i) {
     const int v = threadIdx.x + i * T;
-    return kKeep ? wv : (v < nvec ? __ldg(reinterpret_cast<const uint4*>(p.w) + v) : zero);
+    return kKeep ? wv : (v < nvec ? reinterpret_cast<const uint4*>(p.w)[v] : zero);
   };
   int stage = 0, par = 0;
   uint32_t phase = 0;
   for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x, par ^= 1) {
-    const float rstd = __ldg(p.rstd + row);
+    const float rstd = p.rstd[row];
     // (a wait that gave up leaves its mark in the error word; the rows go on, so that the barriers meet)
     bounded_wait<false>(&full[stage], phase, abort_flag, ERR_ROW_WAIT);
     const uint4* sdy = reinterpret_cast<const uint4*>(row_ring + stage * stage_bytes);

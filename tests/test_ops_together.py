@@ -107,3 +107,53 @@ def test_served_layer():
         tol = tol * (1 + 2.0 ** -8) + ref.abs() * 2.0 ** -8 + 2.0 ** -12 * (xn.abs() @ W.abs().T)
         assert bool(((y.double() - ref).abs() <= tol).all())
     assert qn.device_error() == 0
+
+
+@pytest.mark.parametrize("m", [1, 7, 30, 300])
+def test_kernels_in_a_row_see_one_another(m):
+    """The kernels start before their predecessors end and wait for them on
+    the device: a chain that rewrites its buffers every turn, without a wait
+    on the host, gives what the same chain gives with one after each call."""
+    g = torch.Generator().manual_seed(m)
+    Ws = [wl.normal_bf16(g, (520, D), 0.05).cuda() for _ in range(4)]
+    xs = [wl.normal_bf16(g, (m, D), 1.0).cuda() for _ in range(4)]
+    back = wl.normal_bf16(g, (D, 520), 0.05).cuda()
+    nw = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    w8, b8 = int8.quantize_weight(Ws[0]), int8.quantize_weight(torch.cat([back, back])[:D].contiguous())
+    h = torch.zeros(m, D, dtype=torch.bfloat16, device="cuda")
+    codes, scale = torch.empty(m, D, dtype=torch.int8, device="cuda"), torch.empty(m, device="cuda")
+    y = torch.empty(m, 520, dtype=torch.bfloat16, device="cuda")
+    yq, ys = torch.empty(m, 528, dtype=torch.int8, device="cuda"), torch.empty(m, device="cuda")
+    b8 = int8.Weight(D, 528, torch.cat([b8.codes, b8.codes[:, :8]], 1).contiguous(), b8.scale)
+    yp = torch.zeros(m, 528, dtype=torch.bfloat16, device="cuda")
+
+    def turn(i, wait):
+        done = torch.cuda.synchronize if wait else (lambda: None)
+        int8.quantize(Ws[i % 4], codes=w8.codes, scale=w8.scale)
+        done()
+        norm.forward_int8(xs[i % 4], nw, residual=h, h=h, codes=codes, scale=scale)
+        done()
+        int8.linear(codes, scale, w8, y=y)
+        done()
+        yp[:, :520] = y
+        int8.quantize(yp, codes=yq, scale=ys)
+        done()
+        out = int8.linear(yq, ys, b8)
+        done()
+        total, coef = grads.norm([h, out], 10.0)
+        done()
+        grads.clip([out], coef)
+        done()
+        norm.forward(out, nw, residual=h, h=h)
+        done()
+        return total
+
+    def run(wait):
+        h.zero_()
+        totals = [turn(i, wait) for i in range(40)]
+        return torch.stack(totals), h.clone(), y.clone()
+
+    want = run(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(run(False), want))
+    assert bool(torch.isfinite(want[0]).all()) and qn.device_error() == 0
