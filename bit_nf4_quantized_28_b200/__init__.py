@@ -145,37 +145,43 @@ def _check(status, what):
         raise QNError(status, what)
 
 
-def _arg(t, what, dtype, shape, device=None):
+def _index(t, what):
+    """The index of the cuda device that a call's first tensor is on."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{what}: a cuda tensor is needed, got one on {t.device}")
+    return index
+
+
+def _arg(t, what, dtype, shape, index):
     """Refuses a tensor argument that the library cannot take; returns its
-    address (None for None)."""
+    address (None for None).  index: the call's device."""
     if t is None:
         return None
-    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous() and (
-            device is None or t.device == device):
+    if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
-    raise ValueError(f"{what}: a contiguous {dtype} tensor on {device or 'a cuda device'} is needed, got {t.dtype} on "
-                     f"{t.device}, strides {t.stride()}")
+    raise ValueError(f"{what}: a contiguous {dtype} tensor on cuda:{index} is needed, got {t.dtype} on {t.device}, "
+                     f"strides {t.stride()}")
 
 
-def _out(t, what, dtype, shape, device, like=None):
+def _out(t, what, dtype, shape, index, like=None):
     """An output: the given tensor, checked, or a new one (of the shape of
     `like`, a checked tensor, where that is given: 1 us less); and its address."""
     if t is not None:
-        return t, _arg(t, what, dtype, shape, device)
-    t = torch.empty(shape, dtype=dtype, device=device) if like is None else torch.empty_like(like, dtype=dtype)
+        return t, _arg(t, what, dtype, shape, index)
+    t = torch.empty(shape, dtype=dtype, device=index) if like is None else torch.empty_like(like, dtype=dtype)
     return t, t.data_ptr()
 
 
-def _run(name, device, *args):
-    """Calls `name` with the current stream of `device` (made current for the call)."""
+def _run(name, index, *args):
+    """Calls `name` with the current stream of device `index` (made current for the call)."""
     fn = getattr(lib(), name)
-    index = device.index
     if index == torch.cuda.current_device():
         status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = fn(*args, _raw_stream(index))
     if status != 0:
         _check(status, name)
@@ -410,10 +416,11 @@ def adamw8_step(param, grad, state, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, 
     fp32 value on the device that multiplies the gradient (the clipping
     coefficient of grads.norm)."""
     n = param.numel()
+    index = _index(param, "param")
     if grad_scale is not None and (grad_scale.dtype is not torch.float32 or grad_scale.numel() != 1
-                                   or grad_scale.device != param.device):
+                                   or grad_scale.get_device() != index):
         raise ValueError(f"grad_scale: one fp32 value on {param.device} is needed")
-    _run("qlora_adamw8_step_scaled", param.device, _ptr(param), _ptr(grad), _ptr(grad_scale), n, _ptr(state.m_codes),
+    _run("qlora_adamw8_step_scaled", index, _ptr(param), _ptr(grad), _ptr(grad_scale), n, _ptr(state.m_codes),
          _ptr(state.m_scale), _ptr(state.v_codes), _ptr(state.v_scale), _ptr(param_bf16), float(lr), float(beta1),
          float(beta2), float(eps), float(weight_decay), int(step))
 

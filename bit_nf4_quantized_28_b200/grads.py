@@ -14,7 +14,7 @@ import ctypes
 
 import torch
 
-from . import _run, _TensorList, lib
+from . import _index, _run, _TensorList, lib
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
@@ -28,13 +28,11 @@ class TensorList:
         self.tensors = list(tensors)
         if not self.tensors:
             raise ValueError("at least one tensor is needed")
-        self.device = self.tensors[0].device
+        self.index = _index(self.tensors[0], "tensor 0")
         for i, t in enumerate(self.tensors):
-            if t.dtype not in _DTYPES or not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"tensor {i}: a contiguous float32 or bfloat16 cuda tensor is needed, got {t.dtype} "
-                                 f"on {t.device}, strides {t.stride()}")
-            if t.device != self.device:
-                raise ValueError(f"tensor {i}: is on {t.device}, the others are on {self.device}")
+            if t.dtype not in _DTYPES or t.get_device() != self.index or not t.is_contiguous():
+                raise ValueError(f"tensor {i}: a contiguous float32 or bfloat16 tensor on cuda:{self.index} is needed, "
+                                 f"got {t.dtype} on {t.device}, strides {t.stride()}")
         c = len(self.tensors)
         self._data = (ctypes.c_void_p * c)(*(t.data_ptr() for t in self.tensors))
         self._n = (ctypes.c_int64 * c)(*(t.numel() for t in self.tensors))
@@ -58,7 +56,7 @@ def make_workspace(tensors):
     """Workspace of norm for a list of this length; zeroed once (its first
     256 bytes hold a counter, which every call leaves zero)."""
     tensors = _as_list(tensors)
-    return torch.zeros(workspace_bytes(tensors), dtype=torch.uint8, device=tensors.device)
+    return torch.zeros(workspace_bytes(tensors), dtype=torch.uint8, device=tensors.index)
 
 
 def norm(tensors, max_norm=None, out=None, workspace=None):
@@ -66,15 +64,16 @@ def norm(tensors, max_norm=None, out=None, workspace=None):
     clips it to max_norm (None without max_norm), fp32 scalars on the device.
     out: None or fp32 [2] that receives both."""
     tensors = _as_list(tensors)
-    dev = tensors.device
-    out = torch.empty(2, dtype=torch.float32, device=dev) if out is None else out
-    if out.dtype is not torch.float32 or out.shape != (2,) or out.device != dev or not out.is_contiguous():
-        raise ValueError(f"out: two fp32 values on {dev} are needed")
+    index = tensors.index
+    if out is None:
+        out = torch.empty(2, dtype=torch.float32, device=index)
+    elif out.dtype is not torch.float32 or out.shape != (2,) or out.get_device() != index or not out.is_contiguous():
+        raise ValueError(f"out: two fp32 values on cuda:{index} are needed")
     ws = make_workspace(tensors) if workspace is None else workspace
-    if ws.device != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
-        raise ValueError(f"workspace: a contiguous uint8 tensor on {dev} is needed")
+    if ws.get_device() != index or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"workspace: a contiguous uint8 tensor on cuda:{index} is needed")
     p = out.data_ptr()
-    _run("qlora_grad_norm", dev, tensors.ref, 0.0 if max_norm is None else max_norm, p,
+    _run("qlora_grad_norm", index, tensors.ref, 0.0 if max_norm is None else max_norm, p,
          None if max_norm is None else p + 4, ws.data_ptr(), ws.numel())
     total, coef = out.unbind(0)
     return total, None if max_norm is None else coef
@@ -86,8 +85,9 @@ def clip(tensors, coef, out=None):
     the gradient itself or disjoint from all of them."""
     tensors = _as_list(tensors)
     out = None if out is None else _as_list(out)
-    if coef.dtype is not torch.float32 or coef.numel() != 1 or coef.device != tensors.device:
-        raise ValueError(f"coef: one fp32 value on {tensors.device} is needed")
-    if out is not None and out.device != tensors.device:
-        raise ValueError(f"out: is on {out.device}, the gradients are on {tensors.device}")
-    _run("qlora_grad_clip", tensors.device, tensors.ref, None if out is None else out.ref, coef.data_ptr())
+    index = tensors.index
+    if coef.dtype is not torch.float32 or coef.numel() != 1 or coef.get_device() != index:
+        raise ValueError(f"coef: one fp32 value on cuda:{index} is needed")
+    if out is not None and out.index != index:
+        raise ValueError(f"out: is on cuda:{out.index}, the gradients are on cuda:{index}")
+    _run("qlora_grad_clip", index, tensors.ref, None if out is None else out.ref, coef.data_ptr())

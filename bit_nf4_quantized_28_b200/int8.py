@@ -18,7 +18,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _arg, _out, _run
+from . import _arg, _index, _out, _run
 from . import merge as _merge
 
 BF16, F32, I8 = torch.bfloat16, torch.float32, torch.int8
@@ -39,11 +39,11 @@ def quantize(x, codes=None, scale=None):
     if x.dim() != 2:
         raise ValueError(f"x: [m, k] is needed, got {tuple(x.shape)}")
     m, k = shape = x.shape
-    dev = x.device
-    px = _arg(x, "x", BF16, shape)
-    codes, pc = _out(codes, "codes", I8, shape, dev, x)
-    scale, ps = _out(scale, "scale", F32, (m,), dev)
-    _run("int8_quantize_rows", dev, px, m, k, pc, ps)
+    index = _index(x, "x")
+    px = _arg(x, "x", BF16, shape, index)
+    codes, pc = _out(codes, "codes", I8, shape, index, x)
+    scale, ps = _out(scale, "scale", F32, (m,), index)
+    _run("int8_quantize_rows", index, px, m, k, pc, ps)
     return codes, scale
 
 
@@ -65,9 +65,9 @@ def linear(codes, scale, w, y=None):
     if codes.dim() != 2:
         raise ValueError(f"codes: [m, k] is needed, got {tuple(codes.shape)}")
     m, n, k = codes.shape[0], w.n_out, w.k_in
-    dev = codes.device
-    pc, ps = _arg(codes, "codes", I8, (m, k)), _arg(scale, "scale", F32, (m,), dev)
-    pw, pws = _arg(w.codes, "w.codes", I8, (n, k), dev), _arg(w.scale, "w.scale", F32, (n,), dev)
-    y, py = _out(y, "y", BF16, (m, n), dev)
-    _run("int8_linear_fwd", dev, pc, ps, m, pw, pws, n, k, py)
+    index = _index(codes, "codes")
+    pc, ps = _arg(codes, "codes", I8, (m, k), index), _arg(scale, "scale", F32, (m,), index)
+    pw, pws = _arg(w.codes, "w.codes", I8, (n, k), index), _arg(w.scale, "w.scale", F32, (n,), index)
+    y, py = _out(y, "y", BF16, (m, n), index)
+    _run("int8_linear_fwd", index, pc, ps, m, pw, pws, n, k, py)
     return y

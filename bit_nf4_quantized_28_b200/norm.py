@@ -11,45 +11,43 @@ current stream.  Formulas and rounding: include/qlora_nf4.h.
 
 import torch
 
-from . import _arg, _out, _run, lib
+from . import _arg, _index, _out, _run, lib
 
 BF16, F32 = torch.bfloat16, torch.float32
 
 
 def _inputs(x, weight, residual, h):
-    if x.dim() != 2:
-        raise ValueError(f"x: [m, d] is needed, got {tuple(x.shape)}")
-    dev = x.device
-    px = _arg(x, "x", BF16, x.shape)
-    pr = _arg(residual, "residual", BF16, x.shape, dev)
-    pw = _arg(weight, "weight", BF16, x.shape[1:], dev)
-    if residual is None:
-        return px, None, pw, x, None
-    return px, pr, pw, *_out(h, "h", BF16, x.shape, dev, x)
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x: [m, d] is needed, got {tuple(shape)}")
+    index = _index(x, "x")
+    px = _arg(x, "x", BF16, shape, index)
+    pr = _arg(residual, "residual", BF16, shape, index)
+    pw = _arg(weight, "weight", BF16, shape[1:], index)
+    h, ph = (x, None) if residual is None else _out(h, "h", BF16, shape, index, x)
+    return index, shape, px, pr, pw, h, ph
 
 
 def forward(x, weight, residual=None, eps=1e-5, y=None, h=None, rstd=None):
     """(y, h, rstd): h = x + residual (x itself without a residual), rstd fp32
     [m] for the backward.  Outputs given are written in place; h may be x or
     residual."""
-    px, pr, pw, h, ph = _inputs(x, weight, residual, h)
-    m, d = x.shape
-    dev = x.device
-    y, py = _out(y, "y", BF16, x.shape, dev, x)
-    rstd, ps = _out(rstd, "rstd", F32, (m,), dev)
-    _run("rmsnorm_fwd", dev, px, pr, pw, m, d, eps, ph, py, ps)
+    index, shape, px, pr, pw, h, ph = _inputs(x, weight, residual, h)
+    m, d = shape
+    y, py = _out(y, "y", BF16, shape, index, x)
+    rstd, ps = _out(rstd, "rstd", F32, (m,), index)
+    _run("rmsnorm_fwd", index, px, pr, pw, m, d, eps, ph, py, ps)
     return y, h, rstd
 
 
 def forward_int8(x, weight, residual=None, eps=1e-5, codes=None, scale=None, h=None):
     """(codes, scale, h): the norm's output as int8 codes [m, d] with one fp32
     scale per row; codes * scale stands for y."""
-    px, pr, pw, h, ph = _inputs(x, weight, residual, h)
-    m, d = x.shape
-    dev = x.device
-    codes, pc = _out(codes, "codes", torch.int8, x.shape, dev, x)
-    scale, ps = _out(scale, "scale", F32, (m,), dev)
-    _run("rmsnorm_fwd_int8", dev, px, pr, pw, m, d, eps, ph, pc, ps)
+    index, shape, px, pr, pw, h, ph = _inputs(x, weight, residual, h)
+    m, d = shape
+    codes, pc = _out(codes, "codes", torch.int8, shape, index, x)
+    scale, ps = _out(scale, "scale", F32, (m,), index)
+    _run("rmsnorm_fwd_int8", index, px, pr, pw, m, d, eps, ph, pc, ps)
     return codes, scale, h
 
 
@@ -64,20 +62,21 @@ def backward(dy, h, weight, rstd, dh=None, need_dw=False, out=None, workspace=No
     out: (dx, dw) to write into; dx may be dy or dh."""
     if h.dim() != 2:
         raise ValueError(f"h: [m, d] is needed, got {tuple(h.shape)}")
-    dev = h.device
+    index = _index(h, "h")
     m, d = shape = h.shape
     dx, dw = out if out is not None else (None, None)
     need_dw = dw is not None if out is not None else need_dw
-    args = (_arg(dy, "dy", BF16, shape, dev), _arg(h, "h", BF16, shape), _arg(weight, "weight", BF16, (d,), dev),
-            _arg(rstd, "rstd", F32, (m,), dev), _arg(dh, "dh", BF16, shape, dev))
-    dx, px = _out(dx, "dx", BF16, shape, dev, h)
-    dw, pw = _out(dw, "dw", F32, (d,), dev) if need_dw else (None, None)
+    args = (_arg(dy, "dy", BF16, shape, index), _arg(h, "h", BF16, shape, index),
+            _arg(weight, "weight", BF16, (d,), index), _arg(rstd, "rstd", F32, (m,), index),
+            _arg(dh, "dh", BF16, shape, index))
+    dx, px = _out(dx, "dx", BF16, shape, index, h)
+    dw, pw = _out(dw, "dw", F32, (d,), index) if need_dw else (None, None)
     nbytes = 0
     if need_dw:
-        nbytes = backward_workspace_bytes(m, d) if workspace is None else workspace.numel()
         if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        elif workspace.dtype is not torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace: a contiguous uint8 tensor on {dev} is needed")
-    _run("rmsnorm_bwd", dev, *args, m, d, px, pw, workspace.data_ptr() if need_dw else None, nbytes)
+            workspace = torch.empty(backward_workspace_bytes(m, d), dtype=torch.uint8, device=index)
+        elif workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"workspace: a contiguous uint8 tensor on cuda:{index} is needed")
+        nbytes = workspace.numel()
+    _run("rmsnorm_bwd", index, *args, m, d, px, pw, workspace.data_ptr() if need_dw else None, nbytes)
     return dx, dw
