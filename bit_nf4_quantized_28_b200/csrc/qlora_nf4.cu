@@ -1606,8 +1606,10 @@ qn_status rmsnorm_bwd(const void* dy, const void* h, const void* weight, const f
   if (!set_smem_here(fn, kRowRing, &done[which])) return to_status(cudaErrorInvalidValue);
   cudaError_t e = launch(fn, dim3(static_cast<unsigned>(grid)), dim3(threads), stage * p.stages, st, true, p);
   if (e != cudaSuccess) return to_status(e);
-  return to_status(launch(row_dw_kernel, dim3(static_cast<unsigned>(ceil_div(d, 32))), dim3(32 * kRowDwWarps), 0, st, true,
-                          static_cast<const float*>(p.part), dw, static_cast<int>(grid), static_cast<int>(d)));
+  const int cols = ceil_div(d, 16) <= kRowDwCtas * static_cast<int64_t>(sm_count()) ? 16 : 32;
+  return to_status(launch(cols == 16 ? row_dw_kernel<16> : row_dw_kernel<32>, dim3(static_cast<unsigned>(ceil_div(d, cols))),
+                          dim3(kRowDwThreads), 0, st, true, static_cast<const float*>(p.part), dw, static_cast<int>(grid),
+                          static_cast<int>(d)));
 }
 
 qn_status int8_quantize_rows(const void* x, int64_t m, int64_t k, int8_t* codes, float* scale, qn_stream_t stream) {

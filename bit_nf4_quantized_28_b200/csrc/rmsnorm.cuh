@@ -25,7 +25,7 @@
 // the rate of a plain copy), 8-bit output 36.6 us (6.4 TB/s; of 128-thread
 // CTAs with NV = 4: 42.9 with 256 threads and NV = 2), backward 39.9 us
 // (6.7 TB/s; NV = 2, where NV = 4 took 54.7 with half the threads), with dw
-// 46.5.  Rows to 8 bits 21.9 us (4.6 TB/s): its few bytes per value leave the
+// 45.8.  Rows to 8 bits 21.9 us (4.6 TB/s): its few bytes per value leave the
 // instructions visible (issue slots busy 71 %).  One row of 4096: 1.5 to 2 us.
 #pragma once
 
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_bwd_kernel(RowBwdPara
 // sums of its columns in registers, which leaves too few of them to hold the
 // next rows' loads.  So rows come through a ring in shared memory (bulk
 // copies of dy, h and dh, `stages` rows deep), and each is read there twice.
-// 8192 x 4096: 46.5 us, where loads to registers took 57.4; 2048 x 11008 38.4,
+// 8192 x 4096: 45.8 us, where loads to registers took 57.4; 2048 x 11008 38.4,
 // where they took 58.
 constexpr int kRowBwdMaxStages = 4;
 
@@ -530,27 +530,36 @@ __global__ void __launch_bounds__(1024) row_bwd_dw_kernel(RowBwdParams p) {
   if (abort_word) abort_grace();
 }
 
-// dw = column sums of the CTAs' partial sums, in a fixed order: 16 warps take
-// the rows in turn, 32 columns per CTA, and their sums are added pairwise.
-constexpr int kRowDwWarps = 16;
+// dw = column sums of the CTAs' partial sums, in a fixed order.  A CTA takes
+// kCols columns and as many rows at a time as its threads hold: 16 columns
+// where the CTAs are then resident together, 32 else.  (The backward at 2048 x
+// 4096 took 17.3 us with 16 and 18.0 with 32, 300 x 4096 7.6 and 8.2; 2048 x
+// 11008 40.6 and 38.6, 512 x 32768 53.2 and 48.5.  8 columns gained nothing
+// more.)
+constexpr int kRowDwThreads = 512;
+constexpr int kRowDwCtas = 4;    // resident per SM
 
-__global__ void __launch_bounds__(32 * kRowDwWarps) row_dw_kernel(const float* part, float* dw, int rows, int d) {
-  __shared__ float acc[kRowDwWarps][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+template <int kCols>
+__global__ void __launch_bounds__(kRowDwThreads) row_dw_kernel(const float* part, float* dw, int rows, int d) {
+  constexpr int kGroups = kRowDwThreads / kCols;
+  __shared__ float acc[kGroups][kCols + 1];
+  const int col = threadIdx.x % kCols, group = threadIdx.x / kCols;
+  const int c = blockIdx.x * kCols + col;
   pdl_launch_dependents();
   pdl_wait_primary();
   float s = 0.f;
   if (c < d) {
 #pragma unroll 8
-    for (int r = warp; r < rows; r += kRowDwWarps) s += part[static_cast<int64_t>(r) * d + c];
+    for (int r = group; r < rows; r += kGroups) s += part[static_cast<int64_t>(r) * d + c];
   }
-  acc[warp][lane] = s;
-  for (int n = kRowDwWarps / 2; n > 0; n /= 2) {
-    __syncthreads();
-    if (warp < n) acc[warp][lane] += acc[warp + n][lane];
-  }
-  if (warp == 0 && c < d) dw[c] = acc[0][lane];
+  acc[group][col] = s;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  s = 0.f;
+#pragma unroll
+  for (int r = group; r < kGroups; r += 32 / kCols) s += acc[r][col];
+  if (kCols == 16) s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+  if (group == 0 && c < d) dw[c] = s;
 }
 
 }  // namespace qn
