@@ -25,8 +25,8 @@
 // the rate of a plain copy), 8-bit output 36.6 us (6.4 TB/s; of 128-thread
 // CTAs with NV = 4: 42.9 with 256 threads and NV = 2), backward 39.9 us
 // (6.7 TB/s; NV = 2, where NV = 4 took 54.7 with half the threads), with dw
-// 45.8.  Rows to 8 bits 21.9 us (4.6 TB/s): its few bytes per value leave the
-// instructions visible (issue slots busy 71 %).  One row of 4096: 1.5 to 2 us.
+// 45.8.  Rows to 8 bits 20.4 us (4.9 TB/s): its few bytes per value leave the
+// instructions visible (about 13 to a value).  One row of 4096: 1.4 to 1.9 us.
 #pragma once
 
 #include "bounded_wait.cuh"
@@ -107,6 +107,15 @@ __device__ __forceinline__ void block_sum_max(float& s, uint32_t& a, float* fbuf
   a = __reduce_max_sync(0xFFFFFFFFu, a);
 }
 
+// The maximum alone, in the same way.
+__device__ __forceinline__ uint32_t block_max(uint32_t a, uint32_t* ubuf, int nw) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  a = __reduce_max_sync(0xFFFFFFFFu, a);
+  if (lane == 0) ubuf[warp] = a;
+  __syncthreads();
+  return __reduce_max_sync(0xFFFFFFFFu, lane < nw ? ubuf[lane] : 0u);
+}
+
 // A row of zeros has scale 0 and codes 0; a row with a non-finite value says
 // so in its scale (NaN) and has codes 0.  Outside [2^-60, 2^100], 127 t or
 // 127 / amax could leave fp32's range: such a row is multiplied by a power of
@@ -128,25 +137,57 @@ __device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
   return s;
 }
 
+// Two fp32 values to an instruction, each an ordinary fma.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  return static_cast<uint64_t>(__float_as_uint(hi)) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The largest of three magnitudes.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Codes of 8 values (already multiplied by mult): q = rint(127 t / amax), the
-// quotient rounded to fp32 first (ties to even).  t * inv is within
-// 127 * 2^-24 < 2^-16 of the exact quotient, so the division is needed only
-// where it lies within 2^-14 of a half-integer (one value in 8000): checked
-// once for the 8.  Adding 1.5 * 2^23 rounds to an integer (ties to even)
-// whose low byte is the code.
+// quotient rounded to fp32 first (ties to even).  Adding 1.5 * 2^23 to the
+// product t * inv rounds it to an integer (ties to even) whose low byte is the
+// code, and that product is within 127 * 2^-24 < 2^-16 of the quotient: only
+// where it lies within 2^-14 of a half-integer h could they round apart.
+// There the sign of 127 t - h amax decides, which one fma gives exactly (127 t
+// has 23 bits).  A quotient that is not h does not round to h either: it
+// differs from h by 1 / (254 T) of its size at least, T < 2^16 the significand
+// of t, more than half a step of fp32.  Values of half the largest are such
+// ties, several to a row, so this branch is no rare one: with divisions in it
+// 8192 x 4096 took 21.2 us for 20.4, 333 rows of 11008 with the norm 9.3 for 8.0.
 __device__ __forceinline__ uint2 row_codes(const float (&t)[8], const RowScale& s) {
   constexpr float kMagic = 12582912.f;
   uint32_t c[8];
   float off = 0.f;
+  const uint64_t inv = pair2(s.inv, s.inv), magic = pair2(kMagic, kMagic), minus = pair2(-1.f, -1.f);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float n = fmaf(t[j], s.inv, kMagic);
-    off = fmaxf(off, fabsf(fmaf(t[j], s.inv, kMagic - n)));
-    c[j] = __float_as_uint(n);
+  for (int j = 0; j < 8; j += 2) {
+    const uint64_t v = pair2(t[j], t[j + 1]);
+    const uint64_t n = fma2(v, inv, magic);
+    const uint64_t e = fma2(v, inv, fma2(n, minus, magic));
+    off = max_abs3(off, __uint_as_float(static_cast<uint32_t>(e)), __uint_as_float(static_cast<uint32_t>(e >> 32)));
+    c[j] = static_cast<uint32_t>(n);
+    c[j + 1] = static_cast<uint32_t>(n >> 32);
   }
   if (off > 0.5f - 0x1p-14f) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = __float_as_uint(__fdiv_rn(127.f * t[j], s.amax) + kMagic);
+    for (int j = 0; j < 8; ++j) {
+      const float r = __uint_as_float(c[j]) - kMagic;
+      const float h = r + copysignf(0.5f, fmaf(t[j], s.inv, -r));
+      const float d = fmaf(-h, s.amax, 127.f * t[j]);
+      // (a quarter to d's side; |d| is 0 or at least 2^-90)
+      c[j] = __float_as_uint(h + fminf(fmaxf(d * 0x1p100f, -0.25f), 0.25f) + kMagic);
+    }
   }
   return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040u), __byte_perm(c[2], c[3], 0x0040u), 0x5410u),
                     __byte_perm(__byte_perm(c[4], c[5], 0x0040u), __byte_perm(c[6], c[7], 0x0040u), 0x5410u));
@@ -276,7 +317,6 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_kernel(RowParams p) {
 // and few registers let more rows share an SM.
 template <int NV>
 __global__ void __launch_bounds__(row_max_threads(NV)) row_quant_kernel(RowParams p) {
-  __shared__ float fbuf[2][32];
   __shared__ uint32_t ubuf[2][32];
   const int nvec = p.d >> 3;
   const int T = blockDim.x, nw = T >> 5;
@@ -294,9 +334,7 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_quant_kernel(RowParam
     uint32_t two = 0u;
 #pragma unroll
     for (int i = 0; i < NV; ++i) two = max_vec(two, hv[i]);
-    uint32_t amax = pair_top(two);
-    float none = 0.f;
-    block_sum_max(none, amax, fbuf[par], ubuf[par], nw);
+    const uint32_t amax = block_max(pair_top(two), ubuf[par], nw);
     const RowScale s = row_scale(amax);
     if (threadIdx.x == 0) p.scale[row] = row_scale_value(amax, 1.f);
 #pragma unroll
@@ -313,7 +351,6 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_quant_kernel(RowParam
 // The same for rows too long for a CTA's registers: read twice, the second
 // time from L2.
 __global__ void __launch_bounds__(1024) row_quant_long_kernel(RowParams p) {
-  __shared__ float fbuf[2][32];
   __shared__ uint32_t ubuf[2][32];
   const int nvec = p.d >> 3;
   int par = 0;
@@ -324,9 +361,7 @@ __global__ void __launch_bounds__(1024) row_quant_long_kernel(RowParams p) {
     uint32_t two = 0u;
 #pragma unroll 4
     for (int v = threadIdx.x; v < nvec; v += blockDim.x) two = max_vec(two, x[v]);
-    uint32_t amax = pair_top(two);
-    float none = 0.f;
-    block_sum_max(none, amax, fbuf[par], ubuf[par], blockDim.x >> 5);
+    const uint32_t amax = block_max(pair_top(two), ubuf[par], blockDim.x >> 5);
     const RowScale s = row_scale(amax);
     if (threadIdx.x == 0) p.scale[row] = row_scale_value(amax, 1.f);
 #pragma unroll 2

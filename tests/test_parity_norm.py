@@ -149,6 +149,47 @@ def test_extreme_magnitudes(scale):
     assert np.array_equal(codes.cpu().numpy(), q)
 
 
+def test_codes_at_half_integers():
+    """Every half-integer code, and its neighbours in bf16 (a largest value of
+    127 makes 127 t / amax the value itself)."""
+    half = torch.arange(-126.5, 127, 1.0)
+    ties = half.to(torch.bfloat16)
+    assert torch.equal(ties.float(), half)
+    step = ties.view(torch.int16)
+    row = torch.cat([torch.tensor([127.0, -127.0]).to(torch.bfloat16), ties, (step + 1).view(torch.bfloat16),
+                     (step - 1).view(torch.bfloat16)])
+    x = torch.stack([row, row * 2.0 ** -20, row * 2.0 ** 30, row * 2.0 ** -110, row * 2.0 ** 110])
+    assert x.shape[1] % 8 == 4
+    x = torch.nn.functional.pad(x, (0, 4))
+    q, _ = oracle.quantize(_bits(x))
+    assert np.array_equal(int8.quantize(x.cuda())[0].cpu().numpy(), q)
+    w = torch.ones(x.shape[1], dtype=torch.bfloat16)
+    assert np.array_equal(norm.forward_int8(x.cuda(), w.cuda())[0].cpu().numpy(), q)
+
+
+@pytest.mark.parametrize("a,b", [(255, 255), (129, 131), (251, 193), (181, 181), (255, 129), (128, 128)])
+def test_codes_next_to_half_integers(a, b):
+    """Products h w whose 127 t / amax comes closest to a half-integer, and
+    those that are one: 16-bit significands, found among all pairs."""
+    u, v = np.meshgrid(np.arange(128, 256), np.arange(128, 256), indexing="ij")
+    t, top = (u * v).ravel(), a * b
+    h, w = [a], [float(b)]
+    for s in range(9):
+        # 254 t against odd multiples of top 2^s: zero is a tie, small is close to one
+        r = (254 * t + top * 2 ** s) % (2 * top * 2 ** s)
+        gap = np.minimum(r, 2 * top * 2 ** s - r)
+        for i in np.argsort(gap + 2.0 ** 40 * (t > top * 2 ** s), kind="stable")[:40]:
+            if t[i] <= top * 2 ** s:
+                h.append(int(u.ravel()[i]))
+                w.append(float(v.ravel()[i]) * 2.0 ** -s)
+    n = len(h) // 8 * 8
+    x = torch.tensor([h[:n], [-c for c in h[:n]]], dtype=torch.float32).to(torch.bfloat16)
+    weight = torch.tensor(w[:n], dtype=torch.float32).to(torch.bfloat16)
+    assert weight.float().tolist() == w[:n] and x[0].float().tolist() == h[:n]
+    codes, scale, _ = norm.forward_int8(x.cuda(), weight.cuda(), eps=EPS)
+    _check_codes(codes, scale, _bits(x), weight)
+
+
 def test_non_finite_rows_stay_alone():
     x, _, w = _inputs(6, 512, False, seed=30)
     x[0, 5] = float("nan")
