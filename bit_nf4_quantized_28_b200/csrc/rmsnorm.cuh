@@ -63,6 +63,23 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   }
 }
 
+// Two fp32 values to an instruction, each an ordinary operation.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  return static_cast<uint64_t>(__float_as_uint(hi)) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                     pack_bf16x2(f[6], f[7]));
@@ -80,10 +97,10 @@ __device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b) {
   return r;
 }
 
-// The larger magnitude, or NaN if either is NaN.
-__device__ __forceinline__ float max_abs(float a, float t) {
+// The largest of three magnitudes, or NaN if one is NaN.
+__device__ __forceinline__ float max_abs3_nan(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(t)));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -137,16 +154,6 @@ __device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
   return s;
 }
 
-// Two fp32 values to an instruction, each an ordinary fma.
-__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
-  return static_cast<uint64_t>(__float_as_uint(hi)) << 32 | __float_as_uint(lo);
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // The largest of three magnitudes.
 __device__ __forceinline__ float max_abs3(float a, float b, float c) {
   float r;
@@ -175,7 +182,7 @@ __device__ __forceinline__ uint2 row_codes(const float (&t)[8], const RowScale& 
     const uint64_t v = pair2(t[j], t[j + 1]);
     const uint64_t n = fma2(v, inv, magic);
     const uint64_t e = fma2(v, inv, fma2(n, minus, magic));
-    off = max_abs3(off, __uint_as_float(static_cast<uint32_t>(e)), __uint_as_float(static_cast<uint32_t>(e >> 32)));
+    off = max_abs3(off, lo2(e), hi2(e));
     c[j] = static_cast<uint32_t>(n);
     c[j + 1] = static_cast<uint32_t>(n >> 32);
   }
@@ -240,7 +247,6 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_kernel(RowParams p) {
   for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x, par ^= 1) {
     const int64_t base = row * p.d;
     uint4 hv[NV];
-    float ssq = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * T;
@@ -270,20 +276,25 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_kernel(RowParams p) {
     }
     float t[kInt8 ? NV : 1][8];
     float amax = 0.f;
+    uint64_t sq = 0u;                         // two sums, of the even and the odd columns
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float f[8], wf[8];
       unpack8(hv[i], f);
       if constexpr (kInt8) unpack8(wv[i], wf);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        ssq = fmaf(f[j], f[j], ssq);
+      for (int j = 0; j < 8; j += 2) {
+        const uint64_t f2 = pair2(f[j], f[j + 1]);
+        sq = fma2(f2, f2, sq);
         if constexpr (kInt8) {
-          t[i][j] = f[j] * wf[j];
-          amax = max_abs(amax, t[i][j]);
+          const uint64_t t2 = mul2(f2, pair2(wf[j], wf[j + 1]));
+          t[i][j] = lo2(t2);
+          t[i][j + 1] = hi2(t2);
+          amax = max_abs3_nan(amax, t[i][j], t[i][j + 1]);
         }
       }
     }
+    float ssq = lo2(sq) + hi2(sq);
     uint32_t top = __float_as_uint(amax);
     block_sum_max(ssq, top, fbuf[par], ubuf[par], nw);
     const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(ssq, static_cast<float>(p.d)) + p.eps));
