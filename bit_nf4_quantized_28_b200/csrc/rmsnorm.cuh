@@ -25,8 +25,7 @@
 // the rate of a plain copy), 8-bit output 36.6 us (6.4 TB/s; of 128-thread
 // CTAs with NV = 4: 42.9 with 256 threads and NV = 2), backward 39.9 us
 // (6.7 TB/s; NV = 2, where NV = 4 took 54.7 with half the threads), with dw
-// 45.8.  Rows to 8 bits 20.4 us (4.9 TB/s): its few bytes per value leave the
-// instructions visible (about 13 to a value).  One row of 4096: 1.4 to 1.9 us.
+// 45.8.  Rows to 8 bits 16.1 us (6.3 TB/s).  One row of 4096: 1.2 to 1.9 us.
 #pragma once
 
 #include "bounded_wait.cuh"
@@ -75,6 +74,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
@@ -161,6 +165,14 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
   return r;
 }
 
+constexpr float kMagic = 12582912.f;      // 1.5 * 2^23
+
+// The low bytes of 8 words.
+__device__ __forceinline__ uint2 pack_codes(const uint32_t (&c)[8]) {
+  return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040u), __byte_perm(c[2], c[3], 0x0040u), 0x5410u),
+                    __byte_perm(__byte_perm(c[4], c[5], 0x0040u), __byte_perm(c[6], c[7], 0x0040u), 0x5410u));
+}
+
 // Codes of 8 values (already multiplied by mult): q = rint(127 t / amax), the
 // quotient rounded to fp32 first (ties to even).  Adding 1.5 * 2^23 to the
 // product t * inv rounds it to an integer (ties to even) whose low byte is the
@@ -173,7 +185,6 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
 // ties, several to a row, so this branch is no rare one: with divisions in it
 // 8192 x 4096 took 21.2 us for 20.4, 333 rows of 11008 with the norm 9.3 for 8.0.
 __device__ __forceinline__ uint2 row_codes(const float (&t)[8], const RowScale& s) {
-  constexpr float kMagic = 12582912.f;
   uint32_t c[8];
   float off = 0.f;
   const uint64_t inv = pair2(s.inv, s.inv), magic = pair2(kMagic, kMagic), minus = pair2(-1.f, -1.f);
@@ -196,12 +207,33 @@ __device__ __forceinline__ uint2 row_codes(const float (&t)[8], const RowScale& 
       c[j] = __float_as_uint(h + fminf(fmaxf(d * 0x1p100f, -0.25f), 0.25f) + kMagic);
     }
   }
-  return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040u), __byte_perm(c[2], c[3], 0x0040u), 0x5410u),
-                    __byte_perm(__byte_perm(c[4], c[5], 0x0040u), __byte_perm(c[6], c[7], 0x0040u), 0x5410u));
+  return pack_codes(c);
+}
+
+// The same codes where t is a bf16 value: with 8-bit significands a quotient
+// that is not a half-integer h differs from it by 2^-16 of its size at least.
+// So products with inv made 2^-19 smaller and larger round to the same integer,
+// or, at h itself, to its two neighbours.  The sum of the two rounded products
+// lies between 2^24 and 2^25, where fp32 has even values only: it comes out as
+// twice that integer, or twice the even neighbour, and half of it, its
+// significand, ends in the code.  (8192 x 4096: 20.4 us by row_codes.)
+__device__ __forceinline__ uint2 row_codes_bf16(const float (&t)[8], const RowScale& s) {
+  uint32_t c[8];
+  const float below = s.inv * (1.f - 0x1p-19f), above = s.inv * (1.f + 0x1p-19f);
+  const uint64_t lo = pair2(below, below), hi = pair2(above, above), magic = pair2(kMagic, kMagic);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const uint64_t v = pair2(t[j], t[j + 1]);
+    const uint64_t n = add2(fma2(v, lo, magic), fma2(v, hi, magic));
+    c[j] = static_cast<uint32_t>(n);
+    c[j + 1] = static_cast<uint32_t>(n >> 32);
+  }
+  return pack_codes(c);
 }
 
 // The codes of a row's vector, stored; t is scaled in place where the row's
 // magnitude asks for it.
+template <bool kBf16>
 __device__ __forceinline__ void store_codes(int8_t* out, float (&t)[8], const RowScale& s) {
   uint2 q = make_uint2(0u, 0u);
   if (s.fine) {
@@ -209,7 +241,7 @@ __device__ __forceinline__ void store_codes(int8_t* out, float (&t)[8], const Ro
 #pragma unroll
       for (int j = 0; j < 8; ++j) t[j] *= s.mult;
     }
-    q = row_codes(t, s);
+    q = kBf16 ? row_codes_bf16(t, s) : row_codes(t, s);
   }
   *reinterpret_cast<uint2*>(out) = q;
 }
@@ -304,7 +336,7 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_kernel(RowParams p) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = threadIdx.x + i * T;
-        if (v < nvec) store_codes(p.q + base + 8 * v, t[i], s);
+        if (v < nvec) store_codes<false>(p.q + base + 8 * v, t[i], s);
       }
     } else {
       if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
@@ -354,7 +386,7 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_quant_kernel(RowParam
       if (v >= nvec) continue;
       float f[8];
       unpack8(hv[i], f);
-      store_codes(p.q + base + 8 * v, f, s);
+      store_codes<true>(p.q + base + 8 * v, f, s);
     }
   }
 }
@@ -379,7 +411,7 @@ __global__ void __launch_bounds__(1024) row_quant_long_kernel(RowParams p) {
     for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
       float f[8];
       unpack8(x[v], f);
-      store_codes(p.q + row * p.d + 8 * v, f, s);
+      store_codes<true>(p.q + row * p.d + 8 * v, f, s);
     }
   }
 }
