@@ -182,8 +182,8 @@ __device__ __forceinline__ uint2 pack_codes(const uint32_t (&c)[8]) {
 // has 23 bits).  A quotient that is not h does not round to h either: it
 // differs from h by 1 / (254 T) of its size at least, T < 2^16 the significand
 // of t, more than half a step of fp32.  Values of half the largest are such
-// ties, several to a row, so this branch is no rare one: with divisions in it
-// 8192 x 4096 took 21.2 us for 20.4, 333 rows of 11008 with the norm 9.3 for 8.0.
+// ties, several to a row where all weights are one, so this branch is no rare
+// one: with divisions in it 333 rows of 11008 took 9.3 us for 8.0.
 __device__ __forceinline__ uint2 row_codes(const float (&t)[8], const RowScale& s) {
   uint32_t c[8];
   float off = 0.f;
