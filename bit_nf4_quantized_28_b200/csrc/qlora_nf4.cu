@@ -1470,10 +1470,13 @@ int row_threads(int64_t d, int nv) { return static_cast<int>(round_up(ceil_div(d
 // launching them would take longer than their work (8192 x 256 in one CTA each
 // 8.9 us whatever the output, in 32 per SM 5.3 to 7.1; longer rows lose by it,
 // 20000 x 4096 to bf16 96.8 to 99.9).
+unsigned row_grid(int64_t m, int threads) {
+  return static_cast<unsigned>(std::min<int64_t>(m, threads <= 64 ? int64_t{32} * sm_count() : int64_t{1} << 30));
+}
+
 cudaError_t launch_rows(void (*fn)(RowParams), const RowParams& p, int nv, cudaStream_t st) {
   const int threads = row_threads(p.d, nv);
-  const int64_t grid = std::min<int64_t>(p.m, threads <= 64 ? int64_t{32} * sm_count() : int64_t{1} << 30);
-  return launch(fn, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, st, true, p);
+  return launch(fn, dim3(row_grid(p.m, threads)), dim3(threads), 0, st, true, p);
 }
 
 template <bool kRes, bool kInt8>
@@ -1581,25 +1584,31 @@ qn_status rmsnorm_bwd(const void* dy, const void* h, const void* weight, const f
   p.rstd = rstd;
   p.dh = static_cast<const __nv_bfloat16*>(dh);
   p.dx = static_cast<__nv_bfloat16*>(dx);
-  p.part = static_cast<float*>(ws);
+  p.part = dw ? static_cast<float*>(ws) : nullptr;
   p.m = m;
   p.d = static_cast<int>(d);
-  if (!dw) {
-    // (three rows' registers: few columns per thread)
+  // Without dw a row stays in registers (three rows' registers: few columns per
+  // thread) while two CTAs of it fit an SM; past that, with rows enough to fill
+  // it, the ring is faster (with dh and without: 8192 x 11008 117 and 107 us
+  // for 138 and 136, 2048 x 11008 34 and 31 for 37 and 36, 4096 x 16384 93 and
+  // 77 for 88 and 84; 333 x 11008 takes 9 in registers).
+  if (!dw && (d <= 8192 || m < 8 * static_cast<int64_t>(sm_count()))) {
     const int nv = row_nv(m, d, 256, 2);
     void (*fn)(RowBwdParams) = nv == 1   ? row_bwd_kernel<1>
                                : nv == 2 ? row_bwd_kernel<2>
                                : nv == 4 ? row_bwd_kernel<4>
                                          : row_bwd_kernel<8>;
-    const int64_t grid = std::min<int64_t>(m, int64_t{1} << 30);
-    return to_status(launch(fn, dim3(static_cast<unsigned>(grid)), dim3(row_threads(d, nv)), 0, st, true, p));
+    const int threads = row_threads(d, nv);
+    return to_status(launch(fn, dim3(row_grid(m, threads)), dim3(threads), 0, st, true, p));
   }
   // One vector per thread where 512 threads hold the row, and about 1024
-  // threads per SM: fewer, wider CTAs leave fewer rows of partial sums.
+  // threads per SM: fewer, wider CTAs leave fewer rows of partial sums.  (Two
+  // at most where a row takes more: with three, a ring of two rows of 5120 each
+  // took 77.9 us for 8192 of them, with two of three rows 63.0.)
   int nv = 1;
   while (ceil_div(d / 8, nv) > (nv == 1 ? 512 : 1024)) nv *= 2;
   const int threads = row_threads(d, nv);
-  const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(kRowBwdCtas, 1024 / threads));      // per SM
+  const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(nv == 1 ? kRowBwdCtas : 2, 1024 / threads));      // per SM
   const int64_t grid = std::min<int64_t>(m, ctas * sm_count());
   const size_t stage = static_cast<size_t>(dh ? 6 : 4) * d;
   const size_t room = kRowRing / std::min<int64_t>(ceil_div(grid, sm_count()), ctas);
@@ -1610,7 +1619,7 @@ qn_status rmsnorm_bwd(const void* dy, const void* h, const void* weight, const f
   void (*const fn)(RowBwdParams) = nv == 1 ? row_bwd_dw_kernel<1> : nv == 2 ? row_bwd_dw_kernel<2> : row_bwd_dw_kernel<4>;
   if (!set_smem_here(fn, kRowRing, &done[which])) return to_status(cudaErrorInvalidValue);
   cudaError_t e = launch(fn, dim3(static_cast<unsigned>(grid)), dim3(threads), stage * p.stages, st, true, p);
-  if (e != cudaSuccess) return to_status(e);
+  if (e != cudaSuccess || !dw) return to_status(e);
   const int cols = ceil_div(d, 16) <= kRowDwCtas * static_cast<int64_t>(sm_count()) ? 16 : 32;
   return to_status(launch(cols == 16 ? row_dw_kernel<16> : row_dw_kernel<32>, dim3(static_cast<unsigned>(ceil_div(d, cols))),
                           dim3(kRowDwThreads), 0, st, true, static_cast<const float*>(p.part), dw, static_cast<int>(grid),

@@ -425,10 +425,10 @@ struct RowBwdParams {
   const float* rstd;
   const __nv_bfloat16* dh;    // or null
   __nv_bfloat16* dx;
-  float* part;                // with dw: [gridDim.x, d]
+  float* part;                // ring: [gridDim.x, d], or null without dw
   int64_t m;
   int d;
-  int stages;                 // with dw: rows in flight
+  int stages;                 // ring: rows in flight
 };
 
 template <int NV>
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(row_max_threads(NV)) row_bwd_kernel(RowBwdPara
 // next rows' loads.  So rows come through a ring in shared memory (bulk
 // copies of dy, h and dh, `stages` rows deep), and each is read there twice.
 // 8192 x 4096: 45.8 us, where loads to registers took 57.4; 2048 x 11008 38.4,
-// where they took 58.
+// where they took 58.  Long rows take this way without dw too (part null).
 constexpr int kRowBwdMaxStages = 4;
 
 template <int NV>
@@ -596,11 +596,11 @@ __global__ void __launch_bounds__(1024) row_bwd_dw_kernel(RowBwdParams p) {
       phase ^= 1;
     }
   }
-  float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.d;
+  float* out = p.part ? p.part + static_cast<int64_t>(blockIdx.x) * p.d : nullptr;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = threadIdx.x + i * T;
-    if (v >= nvec) continue;
+    if (v >= nvec || !out) continue;
     float4* o = reinterpret_cast<float4*>(out + 8 * v);
     o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
     o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);

@@ -126,6 +126,35 @@ def test_backward(m, d, need_dw, with_dh):
     assert np.all(np.abs(_f64(dw) - rw) <= adds * U * mag + 1e-38)
 
 
+@pytest.mark.parametrize("m,d", [(5000, 64), (9600, 136), (1300, 8200)])
+def test_more_rows_than_ctas(m, d):
+    """More short rows than the SMs hold CTAs, and long rows enough for the
+    backward's ring."""
+    test_forward(m, d, True)
+    test_forward_int8(m, d, False)
+    test_backward(m, d, False, True)
+    test_backward(m, d, False, False)
+    test_backward(m, d, True, True)
+    test_quantize_rows(m, d)
+    assert qn.device_error() == 0
+
+
+def test_backward_takes_no_workspace_without_dw():
+    """A workspace passed without dw is left as it was."""
+    m, d = 1300, 8200
+    h, _, w = _inputs(m, d, False, seed=40)
+    dy = _bf16(41, m, d)
+    ch, cw, cdy = _cuda(h, w, dy)
+    rstd = norm.forward(ch, cw, eps=EPS)[2]
+    ws = torch.full((norm.backward_workspace_bytes(m, d),), 77, dtype=torch.uint8, device="cuda")
+    dx = torch.empty_like(ch)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert qn.lib().rmsnorm_bwd(cdy.data_ptr(), ch.data_ptr(), cw.data_ptr(), rstd.data_ptr(), None, m, d,
+                                dx.data_ptr(), None, ws.data_ptr(), ws.numel(), stream) == 0
+    assert torch.equal(dx, norm.backward(cdy, ch, cw, rstd)[0])
+    assert bool((ws == 77).all())
+
+
 @pytest.mark.parametrize("m,k", [(1, 8), (3, 64), (5, 11008), (300, 4096), (4096, 264), (2, 32776), (3, 131064)])
 def test_quantize_rows(m, k):
     x, _, _ = _inputs(m, k, False, seed=20)
