@@ -19,10 +19,10 @@
 // vectors of 8 values (16-byte accesses), thread tid the vectors tid + i T.
 // One row per CTA and many CTAs per SM, which cover one another's reductions:
 // persistent CTAs that load the next row ahead measured slower (8192 x 4096,
-// 8-bit output: 43.7 to 49.8 us against 36.6), for the registers they take.
+// 8-bit output: 43.7 to 49.8 us against 36.5), for the registers they take.
 //
 // Measured at 8192 x 4096 with the residual: bf16 output 41.1 us (6.5 TB/s,
-// the rate of a plain copy), 8-bit output 36.6 us (6.4 TB/s; of 128-thread
+// the rate of a plain copy), 8-bit output 36.5 us (6.4 TB/s; of 128-thread
 // CTAs with NV = 4: 42.9 with 256 threads and NV = 2), backward 39.9 us
 // (6.7 TB/s; NV = 2, where NV = 4 took 54.7 with half the threads), with dw
 // 45.8.  Rows to 8 bits 16.1 us (6.3 TB/s).  One row of 4096: 1.2 to 1.9 us.
