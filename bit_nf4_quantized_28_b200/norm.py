@@ -59,7 +59,9 @@ def backward(dy, h, weight, rstd, dh=None, need_dw=False, out=None, workspace=No
     """(dx, dw) of forward: dx bf16 [m, d] is the gradient of x and of
     residual; dw fp32 [d] (None unless need_dw: QLoRA trains the adapters
     only).  dh: None or the gradient that reaches h from the residual stream.
-    out: (dx, dw) to write into; dx may be dy or dh."""
+    out: (dx, dw) to write into; dx may be dy or dh.  workspace: None or one
+    of backward_workspace_bytes(m, d) bytes, which calls that may run at the
+    same time do not share."""
     if h.dim() != 2:
         raise ValueError(f"h: [m, d] is needed, got {tuple(h.shape)}")
     index = _index(h, "h")

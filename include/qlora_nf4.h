@@ -382,7 +382,8 @@ typedef struct {
  * then ignored, else it is finite and >= 0).  An empty list has norm 0.
  * ws: at least qlora_grad_norm_workspace_bytes(count) bytes; its first
  * 256 hold a counter: zero them once when the workspace is made; every call
- * leaves them zero. */
+ * leaves them zero.  Calls that may run at the same time (other streams,
+ * graphs replayed beside one another) need a workspace each. */
 size_t qlora_grad_norm_workspace_bytes(int count);
 qn_status qlora_grad_norm(const qn_tensor_list* grads, float max_norm, float* norm, float* coef,
                           void* ws, size_t ws_bytes, qn_stream_t stream);
@@ -411,8 +412,8 @@ qn_status rmsnorm_fwd(const void* x, const void* residual, const void* weight, i
                       void* h, void* y, float* rstd, qn_stream_t stream);
 
 /* The same norm with its output in 8 bits, one scale per row, for
- * int8_linear_fwd: with t = h * weight (exact in fp32) and amax = max |t| of
- * the row, codes = rint(127 t / amax) (the quotient rounded to fp32, ties to
+ * int8_linear_fwd: with t = h * weight (exact in fp32 down to its smallest
+ * normal, rounded to it below) and amax = max |t| of the row, codes = rint(127 t / amax) (the quotient rounded to fp32, ties to
  * even) and scale = amax * rstd / 127; codes * scale stands for y.
  * codes int8 [m, d], scale fp32 [m].  A row of zeros gets scale 0 and codes
  * 0; a row with a non-finite t gets scale NaN and codes 0 (other rows are
@@ -425,7 +426,9 @@ qn_status rmsnorm_fwd_int8(const void* x, const void* residual, const void* weig
  *   g = dy * weight,  dx = bf16(dh + rstd (g - h rstd^2 mean(g h))),
  *   dw = sum over rows of dy * h * rstd   (fp32 [d]; skipped if dw NULL).
  * dx is the gradient of x and of residual alike; it may be dy or dh.
- * ws: rmsnorm_bwd_workspace_bytes bytes when dw is given (else ignored). */
+ * ws: rmsnorm_bwd_workspace_bytes bytes when dw is given (else ignored);
+ * calls that may run at the same time (other streams, graphs replayed beside
+ * one another) need one each. */
 size_t rmsnorm_bwd_workspace_bytes(int64_t m, int64_t d);
 qn_status rmsnorm_bwd(const void* dy, const void* h, const void* weight, const float* rstd, const void* dh,
                       int64_t m, int64_t d, void* dx, float* dw, void* ws, size_t ws_bytes, qn_stream_t stream);
